@@ -59,6 +59,14 @@ SIGNATURES = [
     ("lowbit_gemm_int4_workspace_bytes", _SZ, [_I64, _I64, _I64]),
     ("lowbit_gemm_int4", _I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _I32, _I64,
                                 _P, _I32, _P, _I32, _I64, _I32, _P, _SZ, _P]),
+    ("lowbit_gemv_int4", _I32, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _I32, _I64,
+                                _P, _I32, _P, _I32, _I64, _I32, _P]),
+    ("lowbit_kv_append", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64,
+                                _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I32, _P, _P]),
+    ("lowbit_kv_read", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    ("lowbit_attention", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64,
+                                _P, _I64, _I64, _P, ctypes.c_float, _I32, _I64, _P, _SZ, _P]),
+    ("lowbit_attention_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64]),
     ("lowbit_quantize", _I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
 ]
 MAX_GROUP = 8
@@ -434,3 +442,220 @@ def gelu(x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> to
     _check(lib().lowbit_gelu(x.data_ptr(), out.data_ptr(), _DT[x.dtype], x.numel(), _stream(stream)),
            "lowbit_gelu")
     return out
+
+
+# ---------------------------------------------------------------------------
+# Decoding: 4-bit products of a few rows, the 8-bit paged key/value cache and
+# attention over it
+# ---------------------------------------------------------------------------
+
+def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """Uninitialised memory for a result written on `stream` (default: the
+    current stream): taken from that stream's pool, so that no pending work
+    of another stream still uses it."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
+              bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, activation=None,
+              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """gemm_int4 for 1 .. 16 rows of x (lowbit_gemv_int4): one launch that
+    reads the codes once, no workspace.
+
+    x: [M, K] fp16/bf16; packed: [N, K/2] uint8; scales, zeros: fp16 [N, K/128]."""
+    for t, nm in ((x, "x"), (packed, "packed"), (scales, "scales"), (zeros, "zeros")):
+        _cuda(t, nm)
+    if x.dim() != 2 or x.stride(1) != 1 or x.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("x must be 2-D float16 or bfloat16 with unit stride along K")
+    M, K = x.shape
+    N = packed.shape[0]
+    packed, scales, zeros = packed.contiguous(), scales.contiguous(), zeros.contiguous()
+    _check_packed(INT4, packed, N, K)
+    for t, nm in ((scales, "scales"), (zeros, "zeros")):
+        if t.dtype != torch.float16 or tuple(t.shape) != (N, K // GROUP):
+            raise ValueError(f"{nm} must be float16 [{N}, {K // GROUP}]")
+    bdt = NONE
+    if bias is not None:
+        _cuda(bias, "bias")
+        bias = bias.contiguous()
+        if bias.numel() != N or bias.dtype not in _DT:
+            raise ValueError(f"bias must hold {N} float16, bfloat16 or float32 values")
+        bdt = _DT[bias.dtype]
+    if out is None:
+        out = _new((M, N), out_dtype or x.dtype, x, stream)
+    elif tuple(out.shape) != (M, N) or out.stride(1) != 1 or out.dtype not in _DT:
+        raise ValueError(f"out must be [{M}, {N}] with unit stride along N")
+    _check(lib().lowbit_gemv_int4(
+        x.data_ptr(), _DT[x.dtype], M, K, x.stride(0), packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+        GROUP, N, _ptr(bias), bdt, out.data_ptr(), _DT[out.dtype], out.stride(0), _ACT[activation],
+        _stream(stream)), "lowbit_gemv_int4")
+    return out
+
+
+class _CacheStruct(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P), ("pages", _I64),
+                ("kv_heads", _I32), ("page", _I32), ("head_dim", _I32)]
+
+
+class KVCache:
+    """A paged cache of keys and values in 8 bits (lowbit_kv_cache).
+
+    k, v: uint8 [pages, kv_heads, page, head_dim], contiguous, in the block
+    layout of include/lowbit.h; k_scale, v_scale: float32 [pages, kv_heads].
+    Made by new_kv_cache, filled by kv_append, read by attention and kv_read."""
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "struct")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        if k.dim() != 4 or k.dtype != torch.uint8 or v.dtype != torch.uint8 or v.shape != k.shape:
+            raise ValueError("k and v must be uint8 [pages, kv_heads, page, head_dim] of one shape")
+        pages, heads, page, d = k.shape
+        if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != (pages, heads)
+                or v_scale.shape != (pages, heads)):
+            raise ValueError(f"k_scale and v_scale must be float32 [{pages}, {heads}]")
+        for t, nm in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
+            _cuda(t, nm)
+            if not t.is_contiguous():
+                raise ValueError(f"{nm} must be contiguous")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                                   pages, heads, page, d)
+
+
+def new_kv_cache(pages: int, kv_heads: int, page: int, head_dim: int, device=None) -> KVCache:
+    """An empty cache: 2 (page * head_dim + 4) bytes a page and head."""
+    dev = torch.device(device or "cuda")
+    k, v = (torch.zeros((pages, kv_heads, page, head_dim), dtype=torch.uint8, device=dev) for _ in range(2))
+    ks, vs = (torch.zeros((pages, kv_heads), dtype=torch.float32, device=dev) for _ in range(2))
+    return KVCache(k, v, ks, vs)
+
+
+def _table(cache: KVCache, block_table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, what: str):
+    """Arguments that every call on the cache begins with, checked."""
+    _cuda(block_table, "block_table")
+    _cuda(cu, "cu_tokens")
+    _cuda(start, what)
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a contiguous int32 tensor [batch, pages of a sequence]")
+    batch, width = block_table.shape
+    if cu.dtype != torch.int32 or cu.shape != (batch + 1,) or not cu.is_contiguous():
+        raise ValueError(f"cu_tokens must be int32 [{batch + 1}]")
+    if start.dtype != torch.int32 or start.shape != (batch,) or not start.is_contiguous():
+        raise ValueError(f"{what} must be int32 [{batch}]")
+    return ctypes.byref(cache.struct), block_table.data_ptr(), width, cu.data_ptr(), start.data_ptr(), batch
+
+
+def _rows3(t: torch.Tensor, shape, dtype, name: str):
+    _cuda(t, name)
+    if tuple(t.shape) != shape or t.dtype != dtype or (t.stride(2) != 1 and t.numel()):
+        raise ValueError(f"{name} must be {dtype} {list(shape)} with unit stride along the last dimension")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor,
+              starts: torch.Tensor, max_tokens: int, q: Optional[torch.Tensor] = None,
+              cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, interleaved: bool = False,
+              q_out: Optional[torch.Tensor] = None, bad_count: Optional[torch.Tensor] = None, stream=None):
+    """Append new keys and values to the cache, rotated by position on the
+    way (lowbit_kv_append); returns the rotated queries when q is given.
+
+    k, v: [T, kv_heads, head_dim] and q: [T, q_heads, head_dim] of one dtype
+    (fp16, bf16, fp32), last dimension contiguous (slices of a fused
+    projection's output do). Sequence b's rows are cu_tokens[b] ..
+    cu_tokens[b+1] - 1 and go to positions starts[b], ...; max_tokens is a
+    host bound on the rows of one sequence. cos, sin: float32 [positions,
+    rot/2], both or none. bad_count: int32 [2], added to: non-finite values
+    (stored as 0) and tokens left out (no page or no position)."""
+    if k.dim() != 3:
+        raise ValueError("k must be [tokens, kv_heads, head_dim]")
+    T, H, D = k.shape
+    if cache.k.shape[1] != H or cache.k.shape[3] != D:
+        raise ValueError(f"the cache holds {cache.k.shape[1]} heads of {cache.k.shape[3]}, k has {H} of {D}")
+    if k.dtype not in _DT:
+        raise ValueError("k must be float16, bfloat16 or float32")
+    head = _table(cache, block_table, cu_tokens, starts, "starts")
+    ka, va = _rows3(k, (T, H, D), k.dtype, "k"), _rows3(v, (T, H, D), k.dtype, "v")
+    if q is not None:
+        Hq = q.shape[1]
+        qa = _rows3(q, (T, Hq, D), k.dtype, "q")
+        if q_out is None:
+            q_out = _new((T, Hq, D), k.dtype, k, stream)
+        qo = _rows3(q_out, (T, Hq, D), k.dtype, "q_out")
+    else:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        Hq, qa, qo = 0, (None, 0, 0), (None, 0, 0)
+    rot = positions = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        for t, nm in ((cos, "cos"), (sin, "sin")):
+            _cuda(t, nm)
+            if t.dim() != 2 or t.dtype != torch.float32 or t.shape != cos.shape or not t.is_contiguous():
+                raise ValueError(f"{nm} must be a contiguous float32 tensor [positions, rot/2]")
+        positions, rot = cos.shape[0], 2 * cos.shape[1]
+    if bad_count is not None:
+        _cuda(bad_count, "bad_count")
+        if bad_count.dtype != torch.int32 or bad_count.numel() != 2 or not bad_count.is_contiguous():
+            raise ValueError("bad_count must be int32 [2]")
+    _check(lib().lowbit_kv_append(*head, T, max_tokens, _DT[k.dtype], *ka, *va, *qa, Hq, *qo, _ptr(cos), _ptr(sin),
+                                  rot, positions, int(interleaved), _ptr(bad_count), _stream(stream)),
+           "lowbit_kv_append")
+    return q_out
+
+
+def kv_read(cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor, starts: torch.Tensor, tokens: int,
+            max_tokens: int, dtype: torch.dtype = torch.bfloat16, out=None,
+            stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The keys and values that the cache holds for a range of each sequence
+    (lowbit_kv_read): rows cu_tokens[b] .. of the two results [tokens,
+    kv_heads, head_dim] are sequence b's tokens starts[b], ... `out` = (k, v)
+    to write into."""
+    if dtype not in _DT:
+        raise ValueError("dtype must be float16, bfloat16 or float32")
+    shape = (tokens, cache.k.shape[1], cache.k.shape[3])
+    head = _table(cache, block_table, cu_tokens, starts, "starts")
+    k, v = (_new(shape, dtype, cache.k, stream), _new(shape, dtype, cache.k, stream)) if out is None else out
+    _check(lib().lowbit_kv_read(*head, tokens, max_tokens, _DT[dtype], *_rows3(k, shape, dtype, "k"),
+                                *_rows3(v, shape, dtype, "v"), _stream(stream)), "lowbit_kv_read")
+    return k, v
+
+
+def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor,
+              lens: torch.Tensor, max_tokens: int, max_len: int, scale: Optional[float] = None, causal: bool = True,
+              window: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False,
+              workspace: Optional[torch.Tensor] = None, stream=None):
+    """Attention of new queries over the cache (lowbit_attention).
+
+    q: [T, q_heads, head_dim] fp16/bf16, last dimension contiguous; q_heads a
+    multiple of the cache's heads. Sequence b has lens[b] tokens in the cache
+    and its queries are rows cu_tokens[b] .. cu_tokens[b+1] - 1, the last ones
+    of it. max_tokens and max_len are host bounds on the queries and the length
+    of one sequence. scale defaults to head_dim ** -0.5; window > 0 keeps the
+    last `window` tokens of each query. Returns out, or (out, lse) with the
+    float32 [T, q_heads] log of the softmax's sum."""
+    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("q must be float16 or bfloat16 [tokens, q_heads, head_dim]")
+    T, Hq, D = q.shape
+    _, H, _, cd = cache.k.shape
+    if cd != D or Hq % H:
+        raise ValueError(f"the cache holds {H} heads of {cd}, q has {Hq} of {D}")
+    head = _table(cache, block_table, cu_tokens, lens, "lens")
+    qa = _rows3(q, (T, Hq, D), q.dtype, "q")
+    if out is None:
+        out = _new((T, Hq, D), q.dtype, q, stream)
+    oa = _rows3(out, (T, Hq, D), q.dtype, "out")
+    lse = _new((T, Hq), torch.float32, q, stream) if return_lse else None
+    need = int(lib().lowbit_attention_workspace_bytes(head[5], T, max_tokens, max_len, Hq, H, D, window))
+    if need and workspace is None:
+        workspace = _new(need, torch.uint8, q, stream)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if size < need:
+        raise ValueError(f"workspace holds {size} bytes, lowbit_attention needs {need}")
+    _check(lib().lowbit_attention(*head, T, max_tokens, max_len, _DT[q.dtype], *qa, Hq, *oa, _ptr(lse),
+                                  D ** -0.5 if scale is None else scale, int(causal), window, _ptr(workspace), size,
+                                  _stream(stream)), "lowbit_attention")
+    return (out, lse) if return_lse else out

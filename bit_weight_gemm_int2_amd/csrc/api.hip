@@ -7,10 +7,12 @@
 #include <cstdlib>
 #include <algorithm>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "../../include/lowbit.h"
 #include "common.h"
+#include "kvcache.h"
 
 namespace lowbit {
 hipError_t launch_pack(int fmt, const int8_t* codes, int64_t N, int64_t K, uint8_t* packed,
@@ -25,6 +27,12 @@ hipError_t launch_gelu(const void* in, void* out, int dtype, int64_t count, hipS
 hipError_t launch_gemm_int4(bool x_bf16, GemmArgs a, int num_cu, int variant, hipStream_t st);
 hipError_t launch_quantize(int fmt, const uint16_t* W, int64_t ldw, int64_t N, int64_t K, uint8_t* packed,
                            uint16_t* scales, int32_t* counter, int variant, hipStream_t st);
+hipError_t launch_gemv_int4(bool x_bf16, const GemmArgs& a, int num_cu, hipStream_t st);
+hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st);
+hipError_t launch_kv_read(const KvReadArgs& g, hipStream_t st);
+hipError_t launch_attention(const AttnArgs& a, bool few, hipStream_t st);
+bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int num_cu,
+                    int* splits, int* split_len);
 int64_t int4_rows(int64_t M);
 size_t int4_workspace(int M, int N, int K, int num_cu, int variant);
 size_t small_workspace_bytes(int M, int N, int K, int num_cu, int variant, int count = 1);
@@ -570,6 +578,274 @@ int32_t lowbit_gemm_int4(const void* X, int32_t x_dtype, int64_t M, int64_t K, i
   a.ldr = lowbit::int4_rows(M);
   hipError_t e = lowbit::launch_gemm_int4(x_dtype == LOWBIT_BF16, a, num_cu, force_variant(), (hipStream_t)stream);
   return e == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+int32_t lowbit_gemv_int4(const void* X, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx, const uint8_t* W_packed,
+                         const void* scales, const void* zeros, int32_t group, int64_t N, const void* bias,
+                         int32_t bias_dtype, void* Y, int32_t y_dtype, int64_t ldy, int32_t activation, void* stream) {
+  if (!zeros) return LOWBIT_ERR_NULL;
+  int64_t rows_max = 0;
+  int32_t st = check_problem(LOWBIT_TERNARY_INT2, X, x_dtype, M, K, ldx, W_packed, scales, group, N, bias,
+                             bias_dtype, Y, y_dtype, ldy, activation, &rows_max);
+  if (st) return st;
+  if (M > 16 || N * (K / 2) > kOffsetSpan || M > rows_max) return LOWBIT_ERR_SHAPE;
+  if (!aligned(zeros, 2)) return LOWBIT_ERR_ALIGN;
+  const int64_t yb = y_span(M, N, ldy, y_dtype), sb = N * (K / 128) * 2;
+  if (overlaps(Y, yb, W_packed, N * (K / 2)) || overlaps(Y, yb, zeros, sb)) return LOWBIT_ERR_OVERLAP;
+  int num_cu = 0;
+  st = current_device(&num_cu);
+  if (st) return st;
+  lowbit::GemmArgs a = make_args(LOWBIT_INT4_ZP, K, ldx, W_packed, scales, N, bias, bias_dtype, y_dtype, ldy,
+                                 activation, nullptr);
+  a.X = (const uint16_t*)X;
+  a.Y = Y;
+  a.M = (int)M;
+  a.Z = (const uint16_t*)zeros;
+  hipError_t e = lowbit::launch_gemv_int4(x_dtype == LOWBIT_BF16, a, num_cu, (hipStream_t)stream);
+  return e == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+}  // extern "C"
+
+namespace {
+
+struct Range {            // the bytes one operand addresses
+  const void* p;
+  int64_t n;
+};
+
+bool any_overlap(Range a, std::initializer_list<Range> others) {
+  for (const Range& o : others)
+    if (overlaps(a.p, a.n, o.p, o.n)) return true;
+  return false;
+}
+
+// Checks shared by the calls on the paged cache.
+int32_t check_cache(const lowbit_kv_cache* c, const int32_t* table, int64_t width, const int32_t* cu,
+                    const int32_t* start, int64_t batch, int64_t tokens, int64_t max_tokens) {
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !cu || !start || (!table && width)) return LOWBIT_ERR_NULL;
+  if (c->pages < 1 || c->kv_heads < 1 || c->kv_heads > 4096 || c->pages >= kMaxDim ||
+      c->pages * c->kv_heads >= kMaxDim)
+    return LOWBIT_ERR_SHAPE;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256) return LOWBIT_ERR_SHAPE;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return LOWBIT_ERR_SHAPE;
+  if (width < 0 || width >= kMaxDim || batch < 1 || batch > 65535 || tokens < 0 || tokens >= kMaxDim ||
+      max_tokens < 1 || max_tokens >= ((int64_t)1 << 30))
+    return LOWBIT_ERR_SHAPE;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      !aligned(table, 4) || !aligned(cu, 4) || !aligned(start, 4))
+    return LOWBIT_ERR_ALIGN;
+  return LOWBIT_OK;
+}
+
+// A dense operand [tokens][heads][D]; one that is written keeps its rows apart.
+int32_t check_rows(const void* p, int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t D, bool written) {
+  if (!p) return LOWBIT_ERR_NULL;
+  if (ts < 0 || hs < 0 || ts >= kMaxDim || hs >= kMaxDim) return LOWBIT_ERR_SHAPE;
+  if (written && !((hs >= D && ts >= (heads - 1) * hs + D) || (ts >= D && hs >= (tokens - 1) * ts + D)))
+    return LOWBIT_ERR_SHAPE;
+  if (!aligned(p, 16) || ts % 8 || hs % 8) return LOWBIT_ERR_ALIGN;
+  return LOWBIT_OK;
+}
+
+Range rows_range(const void* p, int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t D, int32_t dtype) {
+  return {p, ((tokens - 1) * ts + (heads - 1) * hs + D) * (dtype == LOWBIT_F32 ? 4 : 2)};
+}
+
+// A dense operand whose rows may lie between those of another one (queries,
+// keys and values of a token side by side, as a fused projection writes them).
+struct Rows {
+  const void* p;
+  int64_t ts, span;       // bytes from token to token, bytes of one token's heads
+  int64_t n;              // bytes from the first to past the last
+};
+
+Rows rows_of(const void* p, int64_t ts, int64_t hs, int64_t tokens, int64_t heads, int64_t D, int32_t dtype) {
+  const int64_t es = dtype == LOWBIT_F32 ? 4 : 2;
+  return {p, ts * es, ((heads - 1) * hs + D) * es, rows_range(p, ts, hs, tokens, heads, D, dtype).n};
+}
+
+// Equal token strides with every token's heads within one stride: the places
+// within a stride decide; else the whole ranges.
+bool rows_overlap(const Rows& a, const Rows& b) {
+  if (!overlaps(a.p, a.n, b.p, b.n)) return false;
+  if (a.ts != b.ts || a.span > a.ts || b.span > b.ts) return true;
+  int64_t d = (int64_t)((intptr_t)b.p - (intptr_t)a.p) % a.ts;
+  if (d < 0) d += a.ts;
+  return d < a.span || a.ts - d < b.span;
+}
+
+lowbit::KvCache cache_args(const lowbit_kv_cache* c) {
+  return {c->k, c->v, c->k_scale, c->v_scale, c->pages, c->kv_heads, c->page, c->head_dim};
+}
+
+lowbit::KvTable table_args(const int32_t* table, int64_t width, const int32_t* cu, const int32_t* start,
+                           int64_t batch, int64_t tokens, int64_t max_tokens) {
+  return {table, width, cu, start, tokens, (int)batch, (int)std::min(max_tokens, tokens)};
+}
+
+int64_t cache_bytes(const lowbit_kv_cache* c) { return c->pages * c->kv_heads * c->page * (int64_t)c->head_dim; }
+
+}  // namespace
+
+extern "C" {
+
+int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                         const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                         int64_t max_tokens, int32_t dtype, const void* k, int64_t kts, int64_t khs, const void* v,
+                         int64_t vts, int64_t vhs, const void* q, int64_t qts, int64_t qhs, int64_t q_heads,
+                         void* q_out, int64_t ots, int64_t ohs, const float* cos, const float* sin, int64_t rot,
+                         int64_t rope_rows, int32_t interleaved, int32_t* bad_count, void* stream) {
+  if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16 && dtype != LOWBIT_F32) return LOWBIT_ERR_DTYPE;
+  int32_t st = check_cache(cache, block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
+  if (st) return st;
+  const int64_t H = cache->kv_heads, D = cache->head_dim;
+  if (rot < 0 || rot > D || rot % 32 || (rot && (rope_rows < 1 || rope_rows >= kMaxDim))) return LOWBIT_ERR_SHAPE;
+  if ((rot != 0) != (cos != nullptr) || (rot != 0) != (sin != nullptr)) return LOWBIT_ERR_NULL;
+  if ((q == nullptr) != (q_out == nullptr)) return LOWBIT_ERR_NULL;
+  if (q && (q_heads < 1 || q_heads > 65536)) return LOWBIT_ERR_SHAPE;
+  if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(bad_count, 4)) return LOWBIT_ERR_ALIGN;
+  if (!tokens) return LOWBIT_OK;
+  if ((st = check_rows(k, kts, khs, tokens, H, D, false))) return st;
+  if ((st = check_rows(v, vts, vhs, tokens, H, D, false))) return st;
+  if (q && (st = check_rows(q, qts, qhs, tokens, q_heads, D, false))) return st;
+  if (q && (st = check_rows(q_out, ots, ohs, tokens, q_heads, D, true))) return st;
+  const int64_t cb = cache_bytes(cache), sb = cache->pages * H * 4;
+  const Range rk = rows_range(k, kts, khs, tokens, H, D, dtype), rv = rows_range(v, vts, vhs, tokens, H, D, dtype),
+              rq = rows_range(q, qts, qhs, tokens, q_heads, D, dtype),
+              ro = rows_range(q_out, ots, ohs, tokens, q_heads, D, dtype),
+              tab{block_table, batch * table_width * 4}, cu{cu_tokens, (batch + 1) * 4}, sta{starts, batch * 4},
+              co{cos, rope_rows * rot * 2}, si{sin, rope_rows * rot * 2}, ck{cache->k, cb}, cv{cache->v, cb},
+              ks{cache->k_scale, sb}, vs{cache->v_scale, sb}, bad{bad_count, 8};
+  for (const Range& w : {ck, cv, ks, vs, bad})
+    if (any_overlap(w, {rk, rv, rq, tab, cu, sta, co, si})) return LOWBIT_ERR_OVERLAP;
+  const bool in_place = q == q_out && qts == ots && qhs == ohs;
+  const Rows to = rows_of(q_out, ots, ohs, tokens, q_heads, D, dtype);
+  if ((!in_place && rows_overlap(to, rows_of(q, qts, qhs, tokens, q_heads, D, dtype))) ||
+      rows_overlap(to, rows_of(k, kts, khs, tokens, H, D, dtype)) ||
+      rows_overlap(to, rows_of(v, vts, vhs, tokens, H, D, dtype)) || any_overlap(ro, {tab, cu, sta, co, si}) ||
+      any_overlap(ro, {ck, cv, ks, vs, bad}) || any_overlap(bad, {ck, cv, ks, vs}) || any_overlap(ks, {ck, cv, vs}) ||
+      any_overlap(vs, {ck, cv}) || any_overlap(ck, {cv}))
+    return LOWBIT_ERR_OVERLAP;
+  st = current_device(nullptr);
+  if (st) return st;
+  lowbit::KvAppendArgs g{};
+  g.c = cache_args(cache);
+  g.t = table_args(block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
+  g.k = {(void*)k, kts, khs};
+  g.v = {(void*)v, vts, vhs};
+  g.q = {(void*)q, qts, qhs};
+  g.qo = {q_out, ots, ohs};
+  g.q_heads = (int)q_heads;
+  g.dtype = dtype;
+  g.rot = (int)rot;
+  g.inter = interleaved != 0;
+  g.cos = cos;
+  g.sin = sin;
+  g.rope_rows = rope_rows;
+  g.bad = bad_count;
+  return lowbit::launch_kv_append(g, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                       const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                       int64_t max_tokens, int32_t dtype, void* k, int64_t kts, int64_t khs, void* v, int64_t vts,
+                       int64_t vhs, void* stream) {
+  if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16 && dtype != LOWBIT_F32) return LOWBIT_ERR_DTYPE;
+  int32_t st = check_cache(cache, block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
+  if (st) return st;
+  if (!tokens) return LOWBIT_OK;
+  const int64_t H = cache->kv_heads, D = cache->head_dim;
+  if ((st = check_rows(k, kts, khs, tokens, H, D, true))) return st;
+  if ((st = check_rows(v, vts, vhs, tokens, H, D, true))) return st;
+  const int64_t cb = cache_bytes(cache), sb = cache->pages * H * 4;
+  const Range rk = rows_range(k, kts, khs, tokens, H, D, dtype), rv = rows_range(v, vts, vhs, tokens, H, D, dtype);
+  for (const Range& w : {rk, rv})
+    if (any_overlap(w, {{cache->k, cb}, {cache->v, cb}, {cache->k_scale, sb}, {cache->v_scale, sb},
+                        {block_table, batch * table_width * 4}, {cu_tokens, (batch + 1) * 4}, {starts, batch * 4}}))
+      return LOWBIT_ERR_OVERLAP;
+  if (rows_overlap(rows_of(k, kts, khs, tokens, H, D, dtype), rows_of(v, vts, vhs, tokens, H, D, dtype)))
+    return LOWBIT_ERR_OVERLAP;
+  st = current_device(nullptr);
+  if (st) return st;
+  lowbit::KvReadArgs g{};
+  g.c = cache_args(cache);
+  g.t = table_args(block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
+  g.k = {k, kts, khs};
+  g.v = {v, vts, vhs};
+  g.dtype = dtype;
+  return lowbit::launch_kv_read(g, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+static size_t attention_bytes(int splits, int64_t tokens, int64_t q_heads, int64_t D) {
+  return splits > 1 ? (size_t)splits * tokens * q_heads * (D + 2) * sizeof(float) : 0;
+}
+
+size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
+                                        int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window) {
+  if (batch < 1 || tokens < 1 || max_tokens < 1 || max_len < 0 || kv_heads < 1 || q_heads < kv_heads || window < 0 ||
+      batch > 65535 || tokens >= kMaxDim || q_heads > 65536 || max_len > ((int64_t)1 << 30))
+    return 0;
+  int num_cu = 0, splits = 1, len = 0;
+  if (current_device(&num_cu) != LOWBIT_OK) num_cu = 256;   // no gfx950 device: the MI355X's count
+  lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
+                         (int)std::min(window, max_len), num_cu, &splits, &len);
+  return attention_bytes(splits, tokens, q_heads, head_dim);
+}
+
+int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                         const int32_t* cu_tokens, const int32_t* lens, int64_t batch, int64_t tokens,
+                         int64_t max_tokens, int64_t max_len, int32_t dtype, const void* q, int64_t qts, int64_t qhs,
+                         int64_t q_heads, void* out, int64_t ots, int64_t ohs, float* lse, float scale,
+                         int32_t causal, int64_t window, void* workspace, size_t workspace_bytes, void* stream) {
+  if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16) return LOWBIT_ERR_DTYPE;
+  int32_t st = check_cache(cache, block_table, table_width, cu_tokens, lens, batch, tokens, max_tokens);
+  if (st) return st;
+  const int64_t H = cache->kv_heads, D = cache->head_dim;
+  if (q_heads < 1 || q_heads > 65536 || q_heads % H || max_len < 0 || max_len > ((int64_t)1 << 30) || window < 0)
+    return LOWBIT_ERR_SHAPE;
+  if (!tokens) return LOWBIT_OK;
+  max_tokens = std::min(max_tokens, tokens);
+  const int64_t group = q_heads / H;
+  if (max_tokens * group > (int64_t)65535 * 128) return LOWBIT_ERR_SHAPE;   // row tiles of one launch
+  if ((st = check_rows(q, qts, qhs, tokens, q_heads, D, false))) return st;
+  if ((st = check_rows(out, ots, ohs, tokens, q_heads, D, true))) return st;
+  if (!aligned(lse, 4)) return LOWBIT_ERR_ALIGN;
+  const int64_t cb = cache_bytes(cache), sb = cache->pages * H * 4;
+  const Range rq = rows_range(q, qts, qhs, tokens, q_heads, D, dtype),
+              ro = rows_range(out, ots, ohs, tokens, q_heads, D, dtype), rl{lse, tokens * q_heads * 4},
+              rw{workspace, (int64_t)workspace_bytes};
+  for (const Range& w : {ro, rl, rw})
+    if (any_overlap(w, {{cache->k, cb}, {cache->v, cb}, {cache->k_scale, sb}, {cache->v_scale, sb},
+                        {block_table, batch * table_width * 4}, {cu_tokens, (batch + 1) * 4}, {lens, batch * 4}}))
+      return LOWBIT_ERR_OVERLAP;
+  if (any_overlap(ro, {rl, rw}) || any_overlap(rl, {rw, rq}) || any_overlap(rw, {rq}) ||
+      rows_overlap(rows_of(out, ots, ohs, tokens, q_heads, D, dtype), rows_of(q, qts, qhs, tokens, q_heads, D, dtype)))
+    return LOWBIT_ERR_OVERLAP;
+  int num_cu = 0;
+  st = current_device(&num_cu);
+  if (st) return st;
+  lowbit::AttnArgs a{};
+  a.c = cache_args(cache);
+  a.t = table_args(block_table, table_width, cu_tokens, lens, batch, tokens, max_tokens);
+  a.q = {(void*)q, qts, qhs};
+  a.o = {out, ots, ohs};
+  a.lse = lse;
+  a.q_heads = (int)q_heads;
+  a.group = (int)group;
+  a.dtype = dtype;
+  a.scale = scale * 1.44269504088896340736f;
+  a.causal = causal != 0;
+  // a window that holds every token is none for the plan; the mask takes it as it is
+  a.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
+  a.max_len = (int)max_len;
+  const bool few = lowbit::attention_plan(batch, (int)H, a.group, max_tokens, max_len, (int)std::min(window, max_len),
+                                          num_cu, &a.splits, &a.split_len);
+  const size_t need = attention_bytes(a.splits, tokens, q_heads, D);
+  if (need && (!workspace || workspace_bytes < need)) return LOWBIT_ERR_WORKSPACE;
+  if (need && !aligned(workspace, 256)) return LOWBIT_ERR_ALIGN;
+  a.part = (float*)workspace;
+  return lowbit::launch_attention(a, few, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
 }
 
 int32_t lowbit_gelu(const void* in, void* out, int32_t dtype, int64_t count, void* stream) {

@@ -1,0 +1,666 @@
+// Attention of new queries over the 8-bit paged key/value cache (layout:
+// kvcache.h): for a query at position i of its sequence and a head,
+//   o = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q.k_j - max),
+// over the cached tokens j that its mask leaves. k_j = s_k c_k(j) and
+// v_j = s_v c_v(j) with one scale per page and head.
+//
+// Mathematics shared by the kernels:
+//  * Codes are integers of at most 127 and exact in FP16: byte u becomes
+//    0x6400 | u = 1024 + u by one byte permute for two codes, and a packed
+//    add takes 1152 off. Queries are scaled by a power of two per row (exact)
+//    so that BF16 ones keep their range, then rounded to FP16; every product
+//    is exact and sums are FP32.
+//  * Key scales multiply the FP32 scores. Value scales go into the softmax
+//    exponent: with t_j = s_j + log2 s_v(j) (scores in powers of two) and the
+//    running maximum m of t_j, p'_j = 2^(t_j - m) is at most 1, the values'
+//    product needs no scaling per page, and sum_j p_j is the FP32 sum of
+//    p'_j / s_v(j), taken before p' is rounded to FP16 for the matrix
+//    product. One pass over the cache, with the accumulators rescaled only
+//    when a maximum grows.
+//  * Scores are computed transposed (keys as the MFMA's rows), which leaves
+//    every lane with probabilities of one query in just the order in which
+//    the values' product wants them: no exchange between lanes but the
+//    maximum.
+//  * A page whose table entry is no page, and a token that the mask hides,
+//    have t = -inf. A row that keeps nothing gives zeros (and lse = -inf).
+#include <algorithm>
+
+#include "kvcache.h"
+
+namespace lowbit {
+
+namespace {
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+constexpr int PAGES = 264;                 // pages of one segment whose scales are held in LDS
+constexpr float LN2 = 0.69314718055994530942f;
+constexpr float MIN_SCALE = 7.888609052210118e-31f;   // 2^-100: scales below are all-zero blocks
+constexpr float NEG_INF = -__builtin_inff();
+
+struct Pages {
+  int32_t blk[PAGES];                      // page * heads + head, 0 where there is no page
+  float kf[PAGES], lv[PAGES], rv[PAGES];   // key scale * scale, log2 and reciprocal of the value scale
+};
+
+// Two codes (bytes 0, 1 or 2, 3 of w) as FP16.
+__device__ __forceinline__ uint32_t codes2(uint32_t w, uint32_t sel) {
+  const uint32_t p = __builtin_amdgcn_perm(0x64646464u, w, sel);
+  const f16x2 off = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, p) + off);
+}
+__device__ __forceinline__ u32x4 codes8(uint32_t a, uint32_t b) {
+  return u32x4{codes2(a, 0x04010400u), codes2(a, 0x04030402u), codes2(b, 0x04010400u), codes2(b, 0x04030402u)};
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  const f16x2 h = {(_Float16)a, (_Float16)b};
+  return __builtin_bit_cast(uint32_t, h);
+}
+
+// max / sum over the lanes that differ in bit 5 (32) or bits 4, 5 (16) of their
+// number. A lane swap of x with a copy of itself leaves the two halves' values
+// side by side. (The elements are taken as uint32_t first: a bit cast straight
+// from an element of a vector reads element 0 whatever the index.)
+__device__ __forceinline__ float max32(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+  const uint32_t lo = r[0], hi = r[1];
+  return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+}
+__device__ __forceinline__ float max16(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x);
+  const auto r = __builtin_amdgcn_permlane16_swap(b, b, false, false);
+  const uint32_t lo = r[0], hi = r[1];
+  return max32(fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi)));
+}
+__device__ __forceinline__ float sum32(float x) { return x + __shfl_xor(x, 32); }
+__device__ __forceinline__ float sum16(float x) { return sum32(x + __shfl_xor(x, 16)); }
+
+// What one row tile has to do: rows [row0, row0 + rows) of (token, head in
+// group) pairs of one sequence and key/value head, tokens [t0, t1) of its
+// context.
+struct Work {
+  int64_t lo;                              // first row of the sequence in the dense operands
+  int n, rows, row0, len, t0, t1;
+  __device__ __forceinline__ int pos(int row, int group) const { return len - n + row / group; }
+};
+
+__device__ __forceinline__ bool find_work(const AttnArgs& a, int b, int row0, int tile, int split, Work* w) {
+  kv_rows(a.t, b, &w->lo, &w->n);
+  w->rows = min(tile, w->n * a.group - row0);
+  w->row0 = row0;
+  if (w->rows <= 0) return false;
+  const int64_t room = a.t.width * a.c.page;
+  int len = max(0, min(a.t.start[b], a.max_len));
+  w->len = len = (int)min((int64_t)len, room);
+  const int last = w->pos(row0 + w->rows - 1, a.group), first = w->pos(row0, a.group);
+  const int end = a.causal ? max(0, min(len, last + 1)) : len;
+  const int beg = a.window ? max(0, first - a.window + 1) & ~15 : 0;
+  w->t0 = (int)min((int64_t)end, beg + (int64_t)split * a.split_len);
+  w->t1 = (int)min((int64_t)end, beg + ((int64_t)split + 1) * a.split_len);
+  return true;
+}
+
+// Row (token row, head) of the dense operands for row r of the tile.
+__device__ __forceinline__ void row_place(const AttnArgs& a, const Work& w, int h, int r, int64_t* token, int* head) {
+  const int row = w.row0 + r;
+  *token = w.lo + row / a.group;
+  *head = h * a.group + row % a.group;
+}
+
+// Scales of the pages p0 .. p0 + np - 1 of sequence b into LDS.
+__device__ __forceinline__ void load_pages(const AttnArgs& a, int b, int h, int p0, int np, Pages* pg) {
+  for (int i = threadIdx.x; i < np; i += blockDim.x) {
+    const int32_t id = a.t.table[(int64_t)b * a.t.width + p0 + i];
+    const bool there = id >= 0 && id < a.c.pages;
+    const int32_t blk = there ? id * a.c.heads + h : 0;
+    const float ks = a.c.ks[blk], vs = fmaxf(a.c.vs[blk], MIN_SCALE);
+    pg->blk[i] = blk;
+    pg->kf[i] = there ? ks * a.scale : 0.0f;
+    pg->lv[i] = there ? __builtin_amdgcn_logf(vs) : NEG_INF;
+    pg->rv[i] = 1.0f / vs;
+  }
+}
+
+// 8 values of a query as FP32
+template <bool BF16>
+__device__ __forceinline__ void load_q8(const AttnArgs& a, int64_t at, float* x) {
+  const u32x4 w = *(const u32x4*)((const uint16_t*)a.q.p + at);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint16_t v = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+    x[e] = BF16 ? bf16_bits_to_float(v) : half_bits_to_float(v);
+  }
+}
+
+// The power of two that brings a row's largest magnitude into [1, 2), and its inverse.
+__device__ __forceinline__ void row_unit(float top, float* down, float* up) {
+  const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23);        // biased exponent; top >= 0
+  const bool use = e > 1 && e < 253;                                   // else (0, infinite) as it is
+  *down = use ? __builtin_bit_cast(float, (uint32_t)(254 - e) << 23) : 1.0f;
+  *up = use ? __builtin_bit_cast(float, (uint32_t)e << 23) : 1.0f;
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint32_t out2(float x, float y) {
+  return BF16 ? (uint32_t)float_to_bf16_bits(x) | (uint32_t)float_to_bf16_bits(y) << 16 : pack2(x, y);
+}
+
+__device__ __forceinline__ float inverse_sum(float l) { return l != 0.0f ? 1.0f / l : 0.0f; }
+
+__device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t token, int head, float m, float l) {
+  if (a.lse) a.lse[token * a.q_heads + head] = l != 0.0f ? (m + __builtin_amdgcn_logf(l)) * LN2 : NEG_INF;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows (single tokens): 16 rows a workgroup, v_mfma_f32_16x16x32_f16.
+// Bound by reading the cache. Four waves walk 32-token steps of the part in
+// turn, each with its own running maximum, and meet in LDS at the end. A
+// wave reads its keys and values straight into registers (16 bytes a lane,
+// whole kilobytes a wave); the next step's loads are in flight while one is
+// computed.
+// ---------------------------------------------------------------------------
+template <bool BF16, int D>
+__global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
+  constexpr int NI = D / 64, LD = D + 4;
+  __shared__ Pages pg;
+  __shared__ float ml[4][2][16];
+  __shared__ __align__(16) float os[4][16][LD];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, r = lane & 15;
+  const int split = blockIdx.x, h = blockIdx.y % a.c.heads, b = blockIdx.z;
+  Work w;
+  if (!find_work(a, b, 16 * (blockIdx.y / a.c.heads), 16, split, &w)) return;
+  const int shift = 31 - __builtin_clz(a.c.page);
+  const int p0 = w.t0 >> shift;
+
+  float m = NEG_INF, l = 0.0f;
+  f32x4 o[D / 16];
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (w.t0 < w.t1) {
+    load_pages(a, b, h, p0, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
+    // queries: lane (g, r) holds d = 16 (g + 4 i) + 8 half .. + 7 of row r
+    int64_t token;
+    int head;
+    row_place(a, w, h, min(r, w.rows - 1), &token, &head);
+    u32x4 qf[NI][2];
+    float qs;
+    {
+      float x[NI][2][8], top = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          load_q8<BF16>(a, token * a.q.ts + head * a.q.hs + 16 * (g + 4 * i) + 8 * k, x[i][k]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][k][e]));
+        }
+      float down;
+      row_unit(max16(top), &down, &qs);
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) qf[i][k][e] = pack2(x[i][k][2 * e] * down, x[i][k][2 * e + 1] * down);
+    }
+    const int pos = w.pos(w.row0 + min(r, w.rows - 1), a.group);
+    const int hi = a.causal ? min(w.t1, pos + 1) : w.t1, lo = a.window ? pos - a.window + 1 : 0;
+    // tokens that no row of the tile masks
+    const int pos0 = w.pos(w.row0, a.group), pos1 = w.pos(w.row0 + w.rows - 1, a.group);
+    const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = a.window ? pos1 - a.window + 1 : 0;
+    __syncthreads();
+
+    const int last = (w.t1 - 1) & ~15;
+    u32x4 kr[2][NI], vr[2][NI];
+    // block and place of the 16-token tile at t (clamped into the part)
+    auto place = [&](int t, int* page) {
+      t = min(t, last);
+      *page = (t >> shift) - p0;
+      return ((int64_t)pg.blk[*page] << shift) * D + (int64_t)(t & (a.c.page - 1)) * D;
+    };
+    auto load_k = [&](int t) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        int p;
+        const uint8_t* at = a.c.k + place(t + 16 * j, &p) + lane * 16;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) kr[j][i] = *(const u32x4*)(at + 1024 * i);
+      }
+    };
+    auto load_v = [&](int t) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        int p;
+        const uint8_t* at = a.c.v + place(t + 16 * j, &p) + g * 4 * D + r * 16;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) vr[j][i] = *(const u32x4*)(at + 256 * i);
+      }
+    };
+    int t = (w.t0 & ~15) + 32 * wave;
+    if (t < w.t1) {
+      load_k(t);
+      load_v(t);
+    }
+    for (; t < w.t1; t += 128) {
+      f32x4 s[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        s[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            s[j] = mfma16<false>(codes8(kr[j][i][2 * k], kr[j][i][2 * k + 1]), qf[i][k], s[j]);
+      }
+      if (t + 128 < w.t1) load_k(t + 128);
+      float rv[2], mx = NEG_INF;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int p = (min(t + 16 * j, last) >> shift) - p0;
+        const float kf = pg.kf[p] * qs, lv = pg.lv[p];
+        rv[j] = pg.rv[p];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][e] = __builtin_fmaf(s[j][e], kf, lv);
+      }
+      if (t < all_lo || t < w.t0 || t + 32 > all_hi) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int tok = t + 16 * j + 4 * g + e;
+            if (tok < lo || tok < w.t0 || tok >= hi) s[j][e] = NEG_INF;
+          }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx = fmaxf(mx, s[j][e]);
+      mx = max16(mx);
+      if (__any(mx > m)) {
+        const float n = fmaxf(m, mx), f = n > NEG_INF ? __builtin_amdgcn_exp2f(m - n) : 1.0f;
+        m = n;
+        l *= f;
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i] *= f;
+      }
+      const float base = m > NEG_INF ? m : 0.0f;
+      u32x4 pf;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = __builtin_amdgcn_exp2f(s[j][e] - base);
+        l = __builtin_fmaf((p[0] + p[1]) + (p[2] + p[3]), rv[j], l);
+        pf[2 * j] = pack2(p[0], p[1]);
+        pf[2 * j + 1] = pack2(p[2], p[3]);
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) o[4 * i + x] = mfma16<false>(codes8(vr[0][i][x], vr[1][i][x]), pf, o[4 * i + x]);
+      if (t + 128 < w.t1) load_v(t + 128);
+    }
+    l = sum16(l);
+  }
+  // the waves meet: common maximum, then sums in wave order
+  if (g == 0) {
+    ml[wave][0][r] = m;
+    ml[wave][1][r] = l;
+  }
+  __syncthreads();
+  const float top = fmaxf(fmaxf(ml[0][0][r], ml[1][0][r]), fmaxf(ml[2][0][r], ml[3][0][r]));
+  const float f = top > NEG_INF ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+  // lane (g, r): d = 64 i + 16 g + 4 e + x of row r
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *(f32x4*)&os[wave][r][64 * i + 16 * g + 4 * e] =
+          f32x4{o[4 * i][e] * f, o[4 * i + 1][e] * f, o[4 * i + 2][e] * f, o[4 * i + 3][e] * f};
+  __syncthreads();
+  const int row = tid >> 4, d0 = (tid & 15) * 4;
+  if (row >= w.rows) return;
+  float mm = NEG_INF, ll = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) mm = fmaxf(mm, ml[k][0][row]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) ll += ml[k][1][row] * (mm > NEG_INF ? __builtin_amdgcn_exp2f(ml[k][0][row] - mm) : 1.0f);
+  int64_t token;
+  int head;
+  row_place(a, w, h, row, &token, &head);
+  const float inv = a.splits == 1 ? inverse_sum(ll) : 1.0f;
+  const int64_t total = a.t.tokens * a.q_heads, slot = split * total + token * a.q_heads + head;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int d = 64 * i + d0;
+    f32x4 v = *(const f32x4*)&os[0][row][d];
+#pragma unroll
+    for (int k = 1; k < 4; ++k) v += *(const f32x4*)&os[k][row][d];
+    if (a.splits == 1)
+      *(u32x2*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) =
+          u32x2{out2<BF16>(v[0] * inv, v[1] * inv), out2<BF16>(v[2] * inv, v[3] * inv)};
+    else
+      *(f32x4*)(a.part + slot * D + d) = v;
+  }
+  if (d0 == 0) {
+    if (a.splits == 1) {
+      store_lse(a, token, head, mm, ll);
+    } else {
+      float* p = a.part + a.splits * total * D + 2 * slot;
+      p[0] = mm;
+      p[1] = ll;
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows (prompts): 128 rows a workgroup (32 a wave), tiles of 64 tokens,
+// v_mfma_f32_32x32x16_f16. Bound by the matrix and vector instructions.
+// Codes go global -> registers one tile ahead, are converted to FP16 once per
+// workgroup and written to the other of two LDS stages in the order of the
+// MFMA operands (16 consecutive bytes a lane both ways).
+// ---------------------------------------------------------------------------
+namespace many {
+constexpr int ROWS = 128, TOK = 64;
+template <int D> constexpr size_t stage() { return (size_t)TOK * D * 2 * 2; }
+template <int D> constexpr size_t lds() { return 2 * stage<D>(); }
+}  // namespace many
+
+// output dimension of row i of value tile x
+template <int D>
+__device__ __forceinline__ int many_d(int x, int i) {
+  if constexpr (D == 64) return 4 * (i & 15) + x + 2 * (i >> 4);
+  return 128 * (x >> 2) + 4 * i + (x & 3);
+}
+
+template <bool BF16, int D>
+__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_many_kernel(AttnArgs a) {
+  constexpr int TOK = many::TOK, C = D / 16, F = D / 4;
+  constexpr int NK = TOK * C / 256, VP = TOK / 8 * F, NV = (VP + 255) / 256;   // 16-byte key loads; pairs of value loads
+  constexpr int KB = TOK * D * 2;                                      // bytes of keys in a stage
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Pages pg;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int hh = lane >> 5, r = lane & 31;
+  const int h = blockIdx.x % a.c.heads, split = blockIdx.x / a.c.heads, b = blockIdx.z;
+  Work w;
+  // later row tiles see more of the context: they start first
+  if (!find_work(a, b, many::ROWS * (gridDim.y - 1 - blockIdx.y), many::ROWS, split, &w)) return;
+  const int shift = 31 - __builtin_clz(a.c.page);
+
+  const int rr = min(32 * wave + r, w.rows - 1);
+  int64_t token;
+  int head;
+  row_place(a, w, h, rr, &token, &head);
+  u32x4 qf[D / 16];
+  float qs;
+  {
+    float top = 0.0f, x[8], down;
+    const int64_t at = token * a.q.ts + head * a.q.hs + 8 * hh;
+    for (int s = 0; s < D / 16; ++s) {
+      load_q8<BF16>(a, at + 16 * s, x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+    }
+    row_unit(max32(top), &down, &qs);
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) {
+      load_q8<BF16>(a, at + 16 * s, x);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) qf[s][e] = pack2(x[2 * e] * down, x[2 * e + 1] * down);
+    }
+  }
+  const int pos = w.pos(w.row0 + rr, a.group);
+  const int hi = a.causal ? min(w.t1, pos + 1) : w.t1, lo = max(w.t0, a.window ? pos - a.window + 1 : 0);
+  // tokens that no row of this wave masks
+  const int f0 = min(32 * wave, w.rows - 1), f1 = min(32 * wave + 31, w.rows - 1);
+  const int pos0 = w.pos(w.row0 + f0, a.group), pos1 = w.pos(w.row0 + f1, a.group);
+  const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = max(w.t0, a.window ? pos1 - a.window + 1 : 0);
+  // tokens that some row of this wave sees
+  const int any_hi = 32 * wave >= w.rows ? 0 : a.causal ? min(w.t1, pos1 + 1) : w.t1, any_lo = max(w.t0, a.window ? pos0 - a.window + 1 : 0);
+
+  float m = NEG_INF, l = 0.0f;
+  f32x16 o[D / 32];
+#pragma unroll
+  for (int x = 0; x < D / 32; ++x)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[x][e] = 0.0f;
+
+  u32x4 kr[NK], vr[NV][2];
+  const int tbeg = w.t0 & ~15;
+  const int seg_tokens = (PAGES - 8) << shift;                         // tokens whose pages fit the LDS
+  for (int seg = tbeg; seg < w.t1; seg += seg_tokens) {                // a multiple of 64 tokens
+    const int send = min(w.t1, seg + seg_tokens), p0 = seg >> shift, last = (send - 1) & ~15;
+    __syncthreads();
+    load_pages(a, b, h, p0, ((send - 1) >> shift) - p0 + 1, &pg);
+    __syncthreads();
+    auto tile_at = [&](int t) {                                        // bytes of the 16-token tile at t in its array
+      t = min(t, last);
+      return ((int64_t)pg.blk[(t >> shift) - p0] << shift) * D + (int64_t)(t & (a.c.page - 1)) * D;
+    };
+    auto fetch = [&](int t) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {                                   // piece (16-token tile, chunk, token)
+        const int j = tid + 256 * i, sub = j / (16 * C), in = j % (16 * C);
+        kr[i] = *(const u32x4*)(a.c.k + tile_at(t + 16 * sub) + in * 16);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {                                   // piece (step, half, 4 d): quads half and half + 2
+        const int j = tid + 256 * i, sub = j / (2 * F), half = j / F % 2, f = j % F;
+        if (VP < 256 && j >= VP) break;
+        const uint8_t* at = a.c.v + tile_at(t + 16 * sub) + half * 4 * D + f * 16;
+        vr[i][0] = *(const u32x4*)at;
+        vr[i][1] = *(const u32x4*)(at + 8 * D);
+      }
+    };
+    auto stage = [&](uint8_t* to) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {                                   // keys [32-token tile][d / 8][32 tokens][8 d]
+        const int j = tid + 256 * i, sub = j / (16 * C), in = j % (16 * C), c = in >> 4, tk = 16 * (sub & 1) + (in & 15);
+        uint8_t* at = to + (sub >> 1) * (32 * D * 2) + 2 * c * 512 + tk * 16;
+        *(u32x4*)at = codes8(kr[i][0], kr[i][1]);
+        *(u32x4*)(at + 512) = codes8(kr[i][2], kr[i][3]);
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {                                   // values [16-token step][half][tile][32 rows][8 tokens]
+        const int j = tid + 256 * i, sub = j / (2 * F), half = j / F % 2, f = j % F;
+        if (VP < 256 && j >= VP) break;
+        uint8_t* at = to + KB + (sub * 2 + half) * (D * 16);
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int x = D == 64 ? (y & 1) : 4 * (f >> 5) + y, row = D == 64 ? f + 16 * (y >> 1) : f & 31;
+          *(u32x4*)(at + (x * 32 + row) * 16) = codes8(vr[i][0][y], vr[i][1][y]);
+        }
+      }
+    };
+    fetch(seg);
+    stage(smem);
+    __syncthreads();
+    int buf = 0;
+    for (int t = seg; t < send; t += TOK, buf ^= 1) {
+      const bool more = t + TOK < send;
+      if (more) fetch(t + TOK);
+      const uint8_t* ks = smem + buf * many::stage<D>();
+      const uint8_t* vs = ks + KB;
+      if (t < any_hi && t + TOK > any_lo) {
+        f32x16 s[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) s[j][e] = 0.0f;
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            s[j] = mfma32<false>(*(const u32x4*)(ks + j * (32 * D * 2) + (2 * k + hh) * 512 + r * 16), qf[k], s[j]);
+        }
+        float rv[4], mx = NEG_INF;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int p = (min(t + 16 * u, last) >> shift) - p0;
+          const float kf = pg.kf[p] * qs, lv = pg.lv[p];
+          rv[u] = pg.rv[p];
+#pragma unroll
+          for (int e = 8 * (u & 1); e < 8 * (u & 1) + 8; ++e) s[u >> 1][e] = __builtin_fmaf(s[u >> 1][e], kf, lv);
+        }
+        if (t < all_lo || t + TOK > all_hi) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const int tok = t + 32 * j + (e & 3) + 8 * (e >> 2) + 4 * hh;
+              if (tok < lo || tok >= hi) s[j][e] = NEG_INF;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[j][e]);
+        mx = max32(mx);
+        if (__any(mx > m)) {
+          const float n = fmaxf(m, mx), f = n > NEG_INF ? __builtin_amdgcn_exp2f(m - n) : 1.0f;
+          m = n;
+          l *= f;
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) o[x] *= f;
+        }
+        const float base = m > NEG_INF ? m : 0.0f;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          float p[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(s[u >> 1][8 * (u & 1) + e] - base);
+          l = __builtin_fmaf(((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])), rv[u], l);
+          const u32x4 pf = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x)
+            o[x] = mfma32<false>(*(const u32x4*)(vs + (u * 2 + hh) * (D * 16) + (x * 32 + r) * 16), pf, o[x]);
+        }
+      }
+      if (more) stage(smem + (buf ^ 1) * many::stage<D>());
+      __syncthreads();
+    }
+  }
+  l = sum32(l);
+  if (32 * wave + r >= w.rows) return;
+  const int64_t total = a.t.tokens * a.q_heads, slot = split * total + token * a.q_heads + head;
+  const float inv = a.splits == 1 ? inverse_sum(l) : 1.0f;
+  if (hh == 0) {
+    if (a.splits == 1) {
+      store_lse(a, token, head, m, l);
+    } else {
+      float* p = a.part + a.splits * total * D + 2 * slot;
+      p[0] = m;
+      p[1] = l;
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int i = (e & 3) + 8 * (e >> 2) + 4 * hh;
+#pragma unroll
+    for (int x = 0; x < D / 32; x += (D == 64 ? 2 : 4)) {
+      const int d = many_d<D>(x, i);
+      if constexpr (D == 64) {
+        const float v0 = o[x][e] * inv, v1 = o[x + 1][e] * inv;
+        if (a.splits == 1) *(uint32_t*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) = out2<BF16>(v0, v1);
+        else *(f32x2*)(a.part + slot * D + d) = f32x2{v0, v1};
+      } else {
+        const float v0 = o[x][e] * inv, v1 = o[x + 1][e] * inv, v2 = o[x + 2][e] * inv, v3 = o[x + 3][e] * inv;
+        if (a.splits == 1)
+          *(u32x2*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) = u32x2{out2<BF16>(v0, v1), out2<BF16>(v2, v3)};
+        else
+          *(f32x4*)(a.part + slot * D + d) = f32x4{v0, v1, v2, v3};
+      }
+    }
+  }
+}
+
+// Join the parts of the context, one wave a row.
+template <bool BF16, int D>
+__global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t total = a.t.tokens * a.q_heads;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= total) return;
+  const float* ml = a.part + a.splits * total * D;
+  float m = NEG_INF;
+  for (int s = lane; s < a.splits; s += 64) m = fmaxf(m, ml[2 * (s * total + row)]);
+#pragma unroll
+  for (int i = 32; i; i >>= 1) m = fmaxf(m, __shfl_xor(m, i));
+  const float base = m > NEG_INF ? m : 0.0f;
+  constexpr int E = D / 64;
+  float l = 0.0f, v[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = 0.0f;
+  for (int s = 0; s < a.splits; ++s) {
+    const int64_t slot = s * total + row;
+    const float ls = ml[2 * slot + 1];
+    if (ls == 0.0f) continue;                                          // nothing seen there
+    const float f = __builtin_amdgcn_exp2f(ml[2 * slot] - base);
+    l = __builtin_fmaf(ls, f, l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = __builtin_fmaf(a.part[slot * D + e * 64 + lane], f, v[e]);
+  }
+  const float inv = inverse_sum(l);
+  const int64_t token = row / a.q_heads;
+  const int head = (int)(row % a.q_heads);
+  uint16_t* to = (uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs;
+#pragma unroll
+  for (int e = 0; e < E; ++e) to[e * 64 + lane] = (uint16_t)out2<BF16>(v[e] * inv, 0.0f);
+  if (lane == 0) store_lse(a, token, head, m, l);
+}
+
+constexpr int FEW_SPLIT = 4096;            // tokens of a part that PAGES covers at pages of 16 (plus one page of offset)
+
+template <bool BF16, int D>
+hipError_t launch(const AttnArgs& a, bool few, hipStream_t st) {
+  const int rows = a.t.max_tokens * a.group;
+  if (few) {
+    attend_few_kernel<BF16, D><<<dim3(a.splits, a.c.heads * ((rows + 15) / 16), a.t.batch), 256, 0, st>>>(a);
+  } else {
+    constexpr size_t lds = many::lds<D>();
+    if (lds > 64 * 1024) {
+      hipError_t e = hipFuncSetAttribute((const void*)attend_many_kernel<BF16, D>,
+                                         hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+      if (e != hipSuccess) return e;
+    }
+    attend_many_kernel<BF16, D><<<dim3(a.c.heads * a.splits, (rows + many::ROWS - 1) / many::ROWS, a.t.batch), 256, lds, st>>>(a);
+  }
+  if (a.splits > 1)
+    attend_join_kernel<BF16, D><<<dim3((unsigned)((a.t.tokens * a.q_heads + 3) / 4)), 256, 0, st>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Which kernel, and how many parts the context is split into: few-row calls
+// until the parts fill the GPU a few times, many-row calls until the row
+// tiles fill it once.
+bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int num_cu,
+                    int* splits, int* split_len) {
+  const int64_t rows = max_tokens * group;
+  const bool few = rows <= 32;
+  int64_t span = max_len;
+  if (window) span = std::min(span, (int64_t)window + max_tokens + 16);
+  const int64_t tiles = batch * heads * (few ? (rows + 15) / 16 : (rows + many::ROWS - 1) / many::ROWS);
+  const int64_t want = few ? 4 * num_cu : 2 * num_cu, least = few ? 256 : 1024;
+  int64_t n = std::max<int64_t>(1, std::min(want / std::max<int64_t>(tiles, 1), span / least));
+  int64_t len = (span + n - 1) / n;
+  if (few) len = std::min<int64_t>(len, FEW_SPLIT);
+  len = std::max<int64_t>(128, (len + 127) / 128 * 128);
+  *split_len = (int)std::min<int64_t>(len, (int64_t)1 << 30);
+  *splits = (int)std::max<int64_t>(1, (span + len - 1) / len);
+  return few;
+}
+
+hipError_t launch_attention(const AttnArgs& a, bool few, hipStream_t st) {
+  const bool bf = a.dtype == DT_BF16;
+  if (a.c.D == 64) return bf ? launch<true, 64>(a, few, st) : launch<false, 64>(a, few, st);
+  if (a.c.D == 128) return bf ? launch<true, 128>(a, few, st) : launch<false, 128>(a, few, st);
+  return bf ? launch<true, 256>(a, few, st) : launch<false, 256>(a, few, st);
+}
+
+}  // namespace lowbit

@@ -334,6 +334,141 @@ int32_t lowbit_gemm_int4(const void* X, int32_t x_dtype, int64_t M, int64_t K, i
                          void* Y, int32_t y_dtype, int64_t ldy, int32_t activation,
                          void* workspace, size_t workspace_bytes, void* stream);
 
+/* The 4-bit linear for single tokens and small batches, 1 <= M <= 16 rows
+ * (else LOWBIT_ERR_SHAPE): the same Y, arguments and weight layout as
+ * lowbit_gemm_int4, in one launch that reads the codes once, with no
+ * workspace. Accuracy contract per element: |Y - exact| <= 1e-3 *
+ * sum_k |x_k w_k| + 1e-5 + 2^-19 * (16 + max|z|) * sum_k |x_k s_k| (plus half
+ * an output ulp for FP16/BF16 outputs): codes enter as 16 + q. A row of X
+ * that holds an infinity or a NaN gives non-finite values. Deterministic. */
+int32_t lowbit_gemv_int4(const void* X, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                         const uint8_t* W_packed, const void* scales, const void* zeros, int32_t group,
+                         int64_t N, const void* bias, int32_t bias_dtype,
+                         void* Y, int32_t y_dtype, int64_t ldy, int32_t activation, void* stream);
+
+/* A paged cache of keys and values in 8 bits, for attention over tokens seen
+ * before. Every (page, head) is a block of `page` tokens with one FP32 scale
+ * for its keys and one for its values; a value is scale * (u - 128) with a
+ * byte u in 1 .. 255. The bytes of a block lie as the matrix instructions
+ * read them:
+ *   key of token t, dimension d:    byte (t/16) * 16 D + (d/16) * 256 + (t%16) * 16 + d%16
+ *   value of token t, dimension d:  byte (t/4) * 4 D + 4 d + t%4
+ *   k, v              [pages][kv_heads][page][head_dim] bytes, 16-byte aligned
+ *   k_scale, v_scale  [pages][kv_heads] FP32, 4-byte aligned
+ *   page              16, 32, 64, 128 or 256; head_dim 64, 128 or 256
+ *   pages, kv_heads   >= 1, pages * kv_heads < 2^31, kv_heads <= 4096
+ * The struct itself is host memory and read during the call only. Sequence
+ * b's token t lies in page block_table[b * table_width + t / page]; entries
+ * outside 0 .. pages - 1 are no page. Blocks need no initialisation: bytes
+ * and scales of tokens that were never appended are not used. */
+typedef struct {
+  uint8_t* k;
+  uint8_t* v;
+  float* k_scale;
+  float* v_scale;
+  int64_t pages;
+  int32_t kv_heads, page, head_dim;
+} lowbit_kv_cache;
+
+/* Append new tokens to the cache, with their rotation by position on the way.
+ * Sequence b's new tokens are rows cu_tokens[b] .. cu_tokens[b+1] - 1 of the
+ * dense operands and get the positions starts[b], starts[b] + 1, ...
+ *   rotation  of the first `rot` dimensions of every key (and query) at
+ *             position p, with c = cos[p][i], s = sin[p][i], i < rot / 2:
+ *             (x, y) -> (x c - y s, x s + y c) with (x, y) the dimensions
+ *             (i, i + rot/2), or (2i, 2i + 1) when `interleaved` is not 0
+ *   scale     of a block: max(s_old, a / 127), a the largest magnitude of its
+ *             new values, s_old its scale before (0 for a block whose first
+ *             token is new). Scales below 2^-100 become 0.
+ *   codes     128 + rint(r / scale). When a block's scale grows its older
+ *             codes c = u - 128 become rint(c s_old / scale).
+ * FP32 arithmetic; stored values are within 0.5001 scale + 2^-93 of the
+ * (rotated) input, and each later growth of the block adds at most half of
+ * its new scale. The result is a pure function of the input. NaN and infinite
+ * values (after the rotation) are stored as 0 and counted in bad_count[0];
+ * tokens whose page entry is no page, or whose position is not in the tables,
+ * are left out and counted in bad_count[1] (once each; a query without a
+ * position is not written). Two sequences may share a page only when neither
+ * appends to it in this call.
+ *   block_table  int32 [batch][table_width]; cu_tokens int32 [batch + 1],
+ *                rising from 0 to `tokens`; starts int32 [batch], >= 0 (all
+ *                on the device, 4-byte aligned)
+ *   batch        1 .. 65535; tokens >= 0 (0: nothing is done)
+ *   max_tokens   at least the most new tokens of any sequence (host bound of
+ *                the launch; rows past it are not handled), >= 1
+ *   k, v         [tokens][kv_heads][head_dim] of `dtype` (F16, BF16, F32)
+ *   q, q_out     nullable (both or none): [tokens][q_heads][head_dim] of
+ *                `dtype`, rotated into q_out; q_out may be q itself with the
+ *                same strides
+ *                Every dense operand has a token stride and a head stride in
+ *                elements (multiples of 8, >= 0; >= head_dim and apart for
+ *                q_out), last dimension contiguous, 16-byte aligned
+ *   cos, sin     FP32 [rope_rows][rot / 2], 16-byte aligned; NULL with rot = 0
+ *   rot          0 .. head_dim, a multiple of 32
+ *   bad_count    nullable device int32[2], added to (clear it beforehand) */
+int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                         const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                         int64_t max_tokens, int32_t dtype,
+                         const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                         const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                         const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                         void* q_out, int64_t qo_token_stride, int64_t qo_head_stride,
+                         const float* cos, const float* sin, int64_t rot, int64_t rope_rows, int32_t interleaved,
+                         int32_t* bad_count, void* stream);
+
+/* The inverse: rows cu_tokens[b] .. cu_tokens[b+1] - 1 of k and v
+ * ([tokens][kv_heads][head_dim] of `dtype`, strides as q_out above) become the
+ * values that the cache holds for sequence b's tokens starts[b], starts[b] + 1,
+ * ...: the FP32 product scale * (u - 128), rounded to `dtype`; zeros where
+ * there is no page. */
+int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                       const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                       int64_t max_tokens, int32_t dtype,
+                       void* k, int64_t k_token_stride, int64_t k_head_stride,
+                       void* v, int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/* Attention of new queries over the cache (one token a sequence, a few, or
+ * whole prompts; the new tokens' keys and values are in the cache already):
+ *
+ *   out[i, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale * q[i, h] . k_j)
+ *
+ * over the tokens j of query i's sequence that its mask leaves, with the
+ * key/value head h / (q_heads / kv_heads). Sequence b has lens[b] tokens in
+ * the cache; its n = cu_tokens[b+1] - cu_tokens[b] queries are the last n of
+ * them, so query i (from 0) is at position lens[b] - n + i. Token j is seen
+ * when j < lens[b], j <= position (causal not 0), j > position - window
+ * (window > 0), and its page exists. A query that sees nothing gives zeros
+ * (and lse = -infinity).
+ * Scores, softmax and sums are FP32; queries enter the matrix product as FP16
+ * after an exact scaling of each row by a power of two, probabilities as FP16
+ * relative to the row's largest p_j * v_scale, codes exactly. One rounding
+ * to the output type. Deterministic.
+ *   lens         int32 [batch] on the device; lengths above max_len or above
+ *                table_width * page count as that
+ *   max_tokens   at least the most queries of any sequence; max_len at least
+ *                the longest length, 0 .. 2^30 (host bounds of the launch)
+ *   q, out       [tokens][q_heads][head_dim] of dtype (F16 or BF16), strides
+ *                and alignment as in lowbit_kv_append; q_heads a multiple of
+ *                kv_heads
+ *   lse          nullable FP32 [tokens][q_heads]: log of the sum of p_j
+ *   workspace    lowbit_attention_workspace_bytes() bytes, 256-byte aligned,
+ *                NULL when that is 0; no initialisation; calls that can run
+ *                concurrently must not share it
+ * Other arguments as lowbit_kv_append. */
+int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                         const int32_t* cu_tokens, const int32_t* lens, int64_t batch, int64_t tokens,
+                         int64_t max_tokens, int64_t max_len, int32_t dtype,
+                         const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                         void* out, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                         float scale, int32_t causal, int64_t window,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Workspace bytes lowbit_attention needs: the parts' FP32 results where a
+ * long context is split over workgroups, else 0. Depends on the arguments
+ * and the current device's CU count (256 when no gfx950 device is current). */
+size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
+                                        int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window);
+
 /* Several independent linears of one shape in one launch: problem z computes
  *
  *   Y[z] = act( X[z] W[z]^T + bias[z] )
