@@ -449,6 +449,13 @@ def gelu(x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> to
 # attention over it
 # ---------------------------------------------------------------------------
 
+def _queue(stream, device: int) -> int:
+    """The HIP stream of a call: `stream`, or the current stream of the
+    operands' device (taken as a number: a decoding step makes many short
+    calls, and the stream object of torch.cuda.current_stream costs 2 us)."""
+    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+
+
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     """Uninitialised memory for a result written on `stream` (default: the
     current stream): taken from that stream's pool, so that no pending work
@@ -466,16 +473,21 @@ def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
     reads the codes once, no workspace.
 
     x: [M, K] fp16/bf16; packed: [N, K/2] uint8; scales, zeros: fp16 [N, K/128]."""
-    for t, nm in ((x, "x"), (packed, "packed"), (scales, "scales"), (zeros, "zeros")):
-        _cuda(t, nm)
-    if x.dim() != 2 or x.stride(1) != 1 or x.dtype not in (torch.float16, torch.bfloat16):
+    if not (x.is_cuda and packed.is_cuda and scales.is_cuda and zeros.is_cuda):
+        raise ValueError("x, packed, scales and zeros must be GPU tensors")
+    xdt = _DT.get(x.dtype)
+    if x.dim() != 2 or (xdt != F16 and xdt != BF16):
         raise ValueError("x must be 2-D float16 or bfloat16 with unit stride along K")
     M, K = x.shape
+    ldx, unit = x.stride()
+    if unit != 1 and K > 1:
+        raise ValueError("x must be 2-D float16 or bfloat16 with unit stride along K")
     N = packed.shape[0]
     packed, scales, zeros = packed.contiguous(), scales.contiguous(), zeros.contiguous()
-    _check_packed(INT4, packed, N, K)
+    if packed.dtype != torch.uint8 or packed.shape != (N, K // 2):
+        raise ValueError(f"packed must be uint8 [{N}, {K // 2}] for K = {K}, got {packed.dtype} {list(packed.shape)}")
     for t, nm in ((scales, "scales"), (zeros, "zeros")):
-        if t.dtype != torch.float16 or tuple(t.shape) != (N, K // GROUP):
+        if t.dtype != torch.float16 or t.shape != (N, K // GROUP):
             raise ValueError(f"{nm} must be float16 [{N}, {K // GROUP}]")
     bdt = NONE
     if bias is not None:
@@ -485,13 +497,16 @@ def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
             raise ValueError(f"bias must hold {N} float16, bfloat16 or float32 values")
         bdt = _DT[bias.dtype]
     if out is None:
-        out = _new((M, N), out_dtype or x.dtype, x, stream)
-    elif tuple(out.shape) != (M, N) or out.stride(1) != 1 or out.dtype not in _DT:
-        raise ValueError(f"out must be [{M}, {N}] with unit stride along N")
+        out, ldy = _new((M, N), x.dtype if out_dtype is None else out_dtype, x, stream), N
+    else:
+        _cuda(out, "out")
+        if out.shape != (M, N) or out.stride(1) != 1 or out.dtype not in _DT:
+            raise ValueError(f"out must be [{M}, {N}] with unit stride along N")
+        ldy = out.stride(0)
     _check(lib().lowbit_gemv_int4(
-        x.data_ptr(), _DT[x.dtype], M, K, x.stride(0), packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
-        GROUP, N, _ptr(bias), bdt, out.data_ptr(), _DT[out.dtype], out.stride(0), _ACT[activation],
-        _stream(stream)), "lowbit_gemv_int4")
+        x.data_ptr(), xdt, M, K, ldx if M > 1 else K, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
+        GROUP, N, _ptr(bias), bdt, out.data_ptr(), _DT[out.dtype], ldy, _ACT[activation],
+        _queue(stream, x.get_device())), "lowbit_gemv_int4")
     return out
 
 
@@ -507,22 +522,23 @@ class KVCache:
     layout of include/lowbit.h; k_scale, v_scale: float32 [pages, kv_heads].
     Made by new_kv_cache, filled by kv_append, read by attention and kv_read."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "struct")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "kv_heads", "page", "head_dim", "struct", "ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         if k.dim() != 4 or k.dtype != torch.uint8 or v.dtype != torch.uint8 or v.shape != k.shape:
             raise ValueError("k and v must be uint8 [pages, kv_heads, page, head_dim] of one shape")
         pages, heads, page, d = k.shape
+        self.kv_heads, self.page, self.head_dim = heads, page, d
         if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != (pages, heads)
                 or v_scale.shape != (pages, heads)):
             raise ValueError(f"k_scale and v_scale must be float32 [{pages}, {heads}]")
-        for t, nm in ((k, "k"), (v, "v"), (k_scale, "k_scale"), (v_scale, "v_scale")):
-            _cuda(t, nm)
-            if not t.is_contiguous():
-                raise ValueError(f"{nm} must be contiguous")
+        for t in (k, v, k_scale, v_scale):
+            if not (t.is_cuda and t.is_contiguous()):
+                raise ValueError("k, v, k_scale and v_scale must be contiguous GPU tensors")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                    pages, heads, page, d)
+        self.ref = ctypes.byref(self.struct)
 
 
 def new_kv_cache(pages: int, kv_heads: int, page: int, head_dim: int, device=None) -> KVCache:
@@ -533,11 +549,10 @@ def new_kv_cache(pages: int, kv_heads: int, page: int, head_dim: int, device=Non
     return KVCache(k, v, ks, vs)
 
 
-def _table(cache: KVCache, block_table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, what: str):
+def _table(block_table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, what: str):
     """Arguments that every call on the cache begins with, checked."""
-    _cuda(block_table, "block_table")
-    _cuda(cu, "cu_tokens")
-    _cuda(start, what)
+    if not (block_table.is_cuda and cu.is_cuda and start.is_cuda):
+        raise ValueError(f"block_table, cu_tokens and {what} must be GPU tensors")
     if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous int32 tensor [batch, pages of a sequence]")
     batch, width = block_table.shape
@@ -545,14 +560,14 @@ def _table(cache: KVCache, block_table: torch.Tensor, cu: torch.Tensor, start: t
         raise ValueError(f"cu_tokens must be int32 [{batch + 1}]")
     if start.dtype != torch.int32 or start.shape != (batch,) or not start.is_contiguous():
         raise ValueError(f"{what} must be int32 [{batch}]")
-    return ctypes.byref(cache.struct), block_table.data_ptr(), width, cu.data_ptr(), start.data_ptr(), batch
+    return block_table.data_ptr(), width, cu.data_ptr(), start.data_ptr(), batch
 
 
 def _rows3(t: torch.Tensor, shape, dtype, name: str):
-    _cuda(t, name)
-    if tuple(t.shape) != shape or t.dtype != dtype or (t.stride(2) != 1 and t.numel()):
-        raise ValueError(f"{name} must be {dtype} {list(shape)} with unit stride along the last dimension")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    ts, hs, unit = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if not t.is_cuda or t.shape != shape or t.dtype != dtype or (unit != 1 and shape[0]):
+        raise ValueError(f"{name} must be a GPU tensor {dtype} {list(shape)} with unit stride along the last dimension")
+    return t.data_ptr(), ts, hs
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor,
@@ -571,19 +586,22 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
     (stored as 0) and tokens left out (no page or no position)."""
     if k.dim() != 3:
         raise ValueError("k must be [tokens, kv_heads, head_dim]")
-    T, H, D = k.shape
-    if cache.k.shape[1] != H or cache.k.shape[3] != D:
-        raise ValueError(f"the cache holds {cache.k.shape[1]} heads of {cache.k.shape[3]}, k has {H} of {D}")
-    if k.dtype not in _DT:
+    shape, dtype = k.shape, k.dtype
+    T, H, D = shape
+    if cache.kv_heads != H or cache.head_dim != D:
+        raise ValueError(f"the cache holds {cache.kv_heads} heads of {cache.head_dim}, k has {H} of {D}")
+    if dtype not in _DT:
         raise ValueError("k must be float16, bfloat16 or float32")
-    head = _table(cache, block_table, cu_tokens, starts, "starts")
-    ka, va = _rows3(k, (T, H, D), k.dtype, "k"), _rows3(v, (T, H, D), k.dtype, "v")
+    head = _table(block_table, cu_tokens, starts, "starts")
+    ka, va = _rows3(k, shape, dtype, "k"), _rows3(v, shape, dtype, "v")
     if q is not None:
         Hq = q.shape[1]
-        qa = _rows3(q, (T, Hq, D), k.dtype, "q")
+        qa = _rows3(q, (T, Hq, D), dtype, "q")
         if q_out is None:
-            q_out = _new((T, Hq, D), k.dtype, k, stream)
-        qo = _rows3(q_out, (T, Hq, D), k.dtype, "q_out")
+            q_out = _new((T, Hq, D), dtype, k, stream)
+            qo = q_out.data_ptr(), Hq * D, D
+        else:
+            qo = _rows3(q_out, (T, Hq, D), dtype, "q_out")
     else:
         if q_out is not None:
             raise ValueError("q_out without q")
@@ -592,18 +610,20 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        for t, nm in ((cos, "cos"), (sin, "sin")):
-            _cuda(t, nm)
-            if t.dim() != 2 or t.dtype != torch.float32 or t.shape != cos.shape or not t.is_contiguous():
-                raise ValueError(f"{nm} must be a contiguous float32 tensor [positions, rot/2]")
-        positions, rot = cos.shape[0], 2 * cos.shape[1]
+        if cos.dim() != 2 or sin.shape != cos.shape:
+            raise ValueError("cos and sin must be [positions, rot/2]")
+        for t in (cos, sin):
+            if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError("cos and sin must be contiguous float32 GPU tensors")
+        positions, rot = cos.shape
+        rot *= 2
     if bad_count is not None:
         _cuda(bad_count, "bad_count")
         if bad_count.dtype != torch.int32 or bad_count.numel() != 2 or not bad_count.is_contiguous():
             raise ValueError("bad_count must be int32 [2]")
-    _check(lib().lowbit_kv_append(*head, T, max_tokens, _DT[k.dtype], *ka, *va, *qa, Hq, *qo, _ptr(cos), _ptr(sin),
-                                  rot, positions, int(interleaved), _ptr(bad_count), _stream(stream)),
-           "lowbit_kv_append")
+    _check(lib().lowbit_kv_append(cache.ref, *head, T, max_tokens, _DT[dtype], *ka, *va, *qa, Hq, *qo, _ptr(cos),
+                                  _ptr(sin), rot, positions, interleaved, _ptr(bad_count),
+                                  _queue(stream, k.get_device())), "lowbit_kv_append")
     return q_out
 
 
@@ -616,11 +636,17 @@ def kv_read(cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor, 
     to write into."""
     if dtype not in _DT:
         raise ValueError("dtype must be float16, bfloat16 or float32")
-    shape = (tokens, cache.k.shape[1], cache.k.shape[3])
-    head = _table(cache, block_table, cu_tokens, starts, "starts")
-    k, v = (_new(shape, dtype, cache.k, stream), _new(shape, dtype, cache.k, stream)) if out is None else out
-    _check(lib().lowbit_kv_read(*head, tokens, max_tokens, _DT[dtype], *_rows3(k, shape, dtype, "k"),
-                                *_rows3(v, shape, dtype, "v"), _stream(stream)), "lowbit_kv_read")
+    H, D = cache.kv_heads, cache.head_dim
+    shape = (tokens, H, D)
+    head = _table(block_table, cu_tokens, starts, "starts")
+    if out is None:
+        k, v = _new(shape, dtype, cache.k, stream), _new(shape, dtype, cache.k, stream)
+        ka, va = (k.data_ptr(), H * D, D), (v.data_ptr(), H * D, D)
+    else:
+        k, v = out
+        ka, va = _rows3(k, shape, dtype, "k"), _rows3(v, shape, dtype, "v")
+    _check(lib().lowbit_kv_read(cache.ref, *head, tokens, max_tokens, _DT[dtype], *ka, *va,
+                                _queue(stream, cache.k.get_device())), "lowbit_kv_read")
     return k, v
 
 
@@ -637,25 +663,33 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
     of one sequence. scale defaults to head_dim ** -0.5; window > 0 keeps the
     last `window` tokens of each query. Returns out, or (out, lse) with the
     float32 [T, q_heads] log of the softmax's sum."""
-    if q.dim() != 3 or q.dtype not in (torch.float16, torch.bfloat16):
+    dtype = q.dtype
+    if q.dim() != 3 or (dtype != torch.bfloat16 and dtype != torch.float16):
         raise ValueError("q must be float16 or bfloat16 [tokens, q_heads, head_dim]")
-    T, Hq, D = q.shape
-    _, H, _, cd = cache.k.shape
-    if cd != D or Hq % H:
-        raise ValueError(f"the cache holds {H} heads of {cd}, q has {Hq} of {D}")
-    head = _table(cache, block_table, cu_tokens, lens, "lens")
-    qa = _rows3(q, (T, Hq, D), q.dtype, "q")
+    shape = q.shape
+    T, Hq, D = shape
+    H = cache.kv_heads
+    if cache.head_dim != D or Hq % H:
+        raise ValueError(f"the cache holds {H} heads of {cache.head_dim}, q has {Hq} of {D}")
+    head = _table(block_table, cu_tokens, lens, "lens")
+    qa = _rows3(q, shape, dtype, "q")
     if out is None:
-        out = _new((T, Hq, D), q.dtype, q, stream)
-    oa = _rows3(out, (T, Hq, D), q.dtype, "out")
+        out = _new(shape, dtype, q, stream)
+        oa = out.data_ptr(), Hq * D, D
+    else:
+        oa = _rows3(out, shape, dtype, "out")
     lse = _new((T, Hq), torch.float32, q, stream) if return_lse else None
-    need = int(lib().lowbit_attention_workspace_bytes(head[5], T, max_tokens, max_len, Hq, H, D, window))
-    if need and workspace is None:
-        workspace = _new(need, torch.uint8, q, stream)
-    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if size < need:
-        raise ValueError(f"workspace holds {size} bytes, lowbit_attention needs {need}")
-    _check(lib().lowbit_attention(*head, T, max_tokens, max_len, _DT[q.dtype], *qa, Hq, *oa, _ptr(lse),
-                                  D ** -0.5 if scale is None else scale, int(causal), window, _ptr(workspace), size,
-                                  _stream(stream)), "lowbit_attention")
+    L = lib()
+    need = L.lowbit_attention_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window)
+    size = 0
+    if workspace is not None:
+        _cuda(workspace, "workspace")
+        size = workspace.numel() * workspace.element_size()
+        if size < need:
+            raise ValueError(f"workspace holds {size} bytes, lowbit_attention needs {need}")
+    elif need:
+        workspace, size = _new(need, torch.uint8, q, stream), need
+    _check(L.lowbit_attention(cache.ref, *head, T, max_tokens, max_len, _DT[dtype], *qa, Hq, *oa, _ptr(lse),
+                              D ** -0.5 if scale is None else scale, causal, window, _ptr(workspace), size,
+                              _queue(stream, q.get_device())), "lowbit_attention")
     return (out, lse) if return_lse else out
