@@ -17,8 +17,19 @@
 namespace lowbit {
 
 namespace gemv {
-constexpr int MAXWAVES = 16;
+constexpr int MAXWAVES = 12;               // of a workgroup
+constexpr int CU_WAVES = 16;               // waves that a CU holds at the registers of GPW = 3 (124)
+constexpr int RING = 2;                    // tiles in flight a wave (3 to 5 are no faster)
+constexpr int BATCH = 16;                  // tiles between two visits of a chunk of K
+constexpr int slot_bytes(int gpw) { return gpw * 1024 + 512; }   // codes, then scales and zero points (4-byte slots)
+// LDS: rings of the waves, partial tiles [2][waves], biases [2][BATCH][16], running tiles [BATCH] for several chunks
+constexpr size_t lds_bytes(int gpw, int waves, int chunks) {
+  return (size_t)waves * RING * slot_bytes(gpw) + (size_t)2 * waves * 1024 + 2 * BATCH * 64 + (chunks > 1 ? BATCH * 1024 : 0);
 }
+}  // namespace gemv
+
+template <int N>
+__device__ __forceinline__ void wait_loads() { asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory"); }
 
 template <bool BF16>
 __device__ __forceinline__ u32x4 gemv_codes(uint32_t w) {
@@ -38,133 +49,174 @@ __device__ __forceinline__ u32x4 gemv_codes(uint32_t w) {
   return r;
 }
 
-// A workgroup of `blockDim.x / 64` waves owns batches of T tiles of 16
-// columns; wave w holds the activations of GPW groups of K as MFMA operands
-// in registers (the whole of X once per workgroup, over all its batches,
-// while K is at most waves * GPW groups; longer K goes chunk by chunk).
-// Codes: lane (q, c) loads 16 bytes, a quarter of column c's group, so a
-// wave-wide load reads 64 contiguous bytes of 16 columns; a 4 x 4 exchange
-// between the lane groups then gives step s the words 4 s + q, so that the
-// activations' loads cover 64 contiguous bytes of each row too. All code
-// loads of a batch are issued before the first is used. The waves' partial
-// tiles are added in LDS in wave order (deterministic).
-template <bool BF16, int GPW, int T>
-__global__ __launch_bounds__(64 * gemv::MAXWAVES) void gemv_int4_kernel(GemmArgs a) {
+// A workgroup's waves split K: wave w holds the activations of GPW groups as
+// MFMA operands in registers, and the workgroup walks its tiles of 16 columns
+// (blockIdx.x, + gridDim.x, ...), the waves' partial tiles added in LDS in
+// wave order (deterministic). K beyond waves * GPW groups goes chunk by chunk
+// over batches of tiles, so that activations are read once per batch.
+//
+// Bound by the memory pipeline of a CU, so few and wide requests:
+//  * Codes go global -> LDS by DMA into a ring of the wave's own (no barrier
+//    and no registers), RING tiles deep: lane (q, c) fetches a quarter of
+//    column c's group, 64 contiguous bytes of 16 columns an instruction. MFMA
+//    step s then reads word q of quarter s (64 consecutive words), so that
+//    the activations' loads cover 64 contiguous bytes of each row too.
+//  * Scales and zero points: one DMA each for four groups of 16 columns. As
+//    register loads per group they took as long as the codes: 131072 x 2560
+//    at M = 2 took 54 us, 44 without them.
+template <bool BF16, int GPW>
+__global__ __launch_bounds__(64 * gemv::MAXWAVES) void gemv_int4_kernel(GemmArgs a, int chunks) {
+  constexpr int SLOT = gemv::slot_bytes(GPW), RING = gemv::RING, BATCH = gemv::BATCH, LOADS = GPW + 2;
   extern __shared__ __align__(16) uint8_t smem[];
-  f32x4* red = (f32x4*)smem;                                // [waves][T][64]
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6), waves = blockDim.x >> 6;
   const int q = lane >> 4, c16 = lane & 15;
+  uint8_t* ring = smem + wave * RING * SLOT;
+  f32x4* red = (f32x4*)(smem + waves * RING * SLOT);        // [2][waves][64]
+  float* bias = (float*)(red + 2 * waves * 64);             // [2][BATCH][16]
+  f32x4* run = (f32x4*)(bias + 2 * BATCH * 16);             // [BATCH][64]
   const int G = a.K >> 7;
-  const int tiles = (a.N + 15) >> 4, batches = (tiles + T - 1) / T;
-  const int per = waves * GPW;                              // groups in one chunk
+  const int tiles = (a.N + 15) >> 4, nb = gridDim.x;
+  const int te = (tiles - 1 - (int)blockIdx.x) / nb + 1;    // tiles of this workgroup
+  const int items = te * chunks;
   const uint16_t* xrow = a.X + (int64_t)min(c16, a.M - 1) * a.ldx + 8 * q;
   constexpr uint32_t one = BF16 ? 0x3F803F80u : 0x3C003C00u;
   const u32x4 ones = {one, one, one, one};
   const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
 
+  // order of the work: batch of tiles, chunk of K, tile
+  struct Item { int tile, chunk, first; };
+  auto advance = [&](Item& i) __attribute__((always_inline)) {
+    if (++i.tile == min(i.first + BATCH, te)) {
+      if (++i.chunk == chunks) {
+        i.chunk = 0;
+        i.first = i.tile;
+      } else {
+        i.tile = i.first;
+      }
+    }
+  };
+  // first group of this wave in a chunk; groups past the end repeat the last one (and count for nothing)
+  auto group0 = [&](int chunk) __attribute__((always_inline)) { return (chunk * waves + wave) * GPW; };
+  auto fetch = [&](const Item& i, int slot) __attribute__((always_inline)) {
+    const uint32_t n = min((blockIdx.x + i.tile * nb) * 16 + c16, (uint32_t)a.N - 1);
+    const int gw = group0(i.chunk);
+    const uint32_t wo = n * ((uint32_t)a.K >> 1) + 16 * q;  // codes span less than 4 GiB
+    const uint32_t so = (n * (uint32_t)G + (uint32_t)min(gw + min(q, GPW - 1), G - 1)) * 2;
+    const uint32_t to = lds_addr(ring + slot * SLOT);
+#pragma unroll
+    for (int u = 0; u < GPW; ++u) dma_lds16(a.W, wo + (uint32_t)min(gw + u, G - 1) * 64, to + u * 1024);
+    dma_lds2(a.S, so, to + GPW * 1024);
+    dma_lds2(a.Z, so, to + GPW * 1024 + 256);
+  };
+
   u32x4 xf[GPW][4];
   f32x4 sx[GPW];
-  for (int batch = blockIdx.x; batch < batches; batch += gridDim.x) {
-    f32x4 acc[T];
+  Item in{0, 0, 0}, at{0, 0, 0};                            // next to fetch, next to compute
 #pragma unroll
-    for (int t = 0; t < T; ++t) acc[t] = zero;
-    for (int g0 = 0; g0 < G; g0 += per) {
-      const int gw = g0 + wave * GPW;                       // first group of this wave
-      const int ng = min(GPW, G - gw);                      // may be <= 0: nothing to add
-      if (ng > 0) {
-        u32x4 cw[T][GPW];
-        uint32_t sr[T], zr[T];
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-          const int64_t n = min((batch * T + t) * 16 + c16, a.N - 1);
-          const uint8_t* wp = a.W + n * (a.K >> 1) + 16 * q;
-#pragma unroll
-          for (int u = 0; u < GPW; ++u) cw[t][u] = *(const u32x4*)(wp + (gw + min(u, ng - 1)) * 64);
-          const int64_t at = n * G + gw + min(q, ng - 1);
-          sr[t] = a.S[at];
-          zr[t] = a.Z[at];
+  for (int r = 0; r < RING; ++r)
+    if (r < items) {
+      fetch(in, r);
+      advance(in);
+    }
+  int slot = 0, buf = 0;
+  for (int i = 0; i < items; ++i) {
+    const int gw = group0(at.chunk), tb = at.tile - at.first;
+    if (tb == 0) {                                          // wave-uniform: a new batch or chunk
+      if (at.chunk == 0 && a.bias) {
+        for (int k = tid; k < BATCH * 16; k += blockDim.x) {
+          const int nk = (blockIdx.x + (at.first + (k >> 4)) * nb) * 16 + (k & 15);
+          bias[((at.first / BATCH) & 1) * BATCH * 16 + k] =
+              (at.first + (k >> 4) < te && nk < a.N) ? load_bias(a.bias, a.bias_dtype, nk) : 0.0f;
         }
-        if (batch == (int)blockIdx.x || per < G) {
+      }
+      if (i == 0 || chunks > 1) {
 #pragma unroll
-          for (int u = 0; u < GPW; ++u)
+        for (int u = 0; u < GPW; ++u)
 #pragma unroll
-            for (int s = 0; s < 4; ++s) xf[u][s] = *(const u32x4*)(xrow + (gw + min(u, ng - 1)) * 128 + 32 * s);
+          for (int s = 0; s < 4; ++s) xf[u][s] = *(const u32x4*)(xrow + (int64_t)min(gw + u, G - 1) * 128 + 32 * s);
 #pragma unroll
-          for (int u = 0; u < GPW; ++u) {
-            sx[u] = zero;
+        for (int u = 0; u < GPW; ++u) {
+          sx[u] = zero;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) sx[u] = mfma16<BF16>(xf[u][s], ones, sx[u]);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < T; ++t) {
-#pragma unroll
-          for (int u = 0; u < GPW; ++u) {
-            auto x = __builtin_amdgcn_permlane32_swap(cw[t][u][0], cw[t][u][2], false, false);
-            auto y = __builtin_amdgcn_permlane32_swap(cw[t][u][1], cw[t][u][3], false, false);
-            auto e = __builtin_amdgcn_permlane16_swap(x[0], y[0], false, false);
-            auto o = __builtin_amdgcn_permlane16_swap(x[1], y[1], false, false);
-            const uint32_t w[4] = {e[0], e[1], o[0], o[1]};
-            f32x4 p = zero;
-#pragma unroll
-            for (int s = 0; s < 4; ++s) p = mfma16<BF16>(xf[u][s], gemv_codes<BF16>(w[s]), p);
-            // the scale and zero point of group gw + u sit in lane group u
-            const float s_ = half_bits_to_float((uint16_t)__shfl((int)sr[t], 16 * u + c16));
-            const float z_ = half_bits_to_float((uint16_t)__shfl((int)zr[t], 16 * u + c16));
-            if (u < ng) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                acc[t][i] = __builtin_fmaf(s_, __builtin_fmaf(-(16.0f + z_), sx[u][i], p[i]), acc[t][i]);
-            }
-          }
+          for (int s = 0; s < 4; ++s) sx[u] = mfma16<BF16>(xf[u][s], ones, sx[u]);
         }
       }
     }
-    if (waves > 1) {
+    // this item's loads are done; those of the next RING - 1 items may be in flight
+    if (items - i >= RING) wait_loads<(RING - 1) * LOADS>();
+    else wait_loads<0>();
+    const uint8_t* from = ring + slot * SLOT;
+    f32x4 acc = zero;
 #pragma unroll
-      for (int t = 0; t < T; ++t) red[(wave * T + t) * 64 + lane] = acc[t];
+    for (int u = 0; u < GPW; ++u) {
+      f32x4 p = zero;
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+        p = mfma16<BF16>(xf[u][s], gemv_codes<BF16>(*(const uint32_t*)(from + u * 1024 + (s * 16 + c16) * 16 + q * 4)), p);
+      const float sc = half_bits_to_float(*(const uint16_t*)(from + GPW * 1024 + (u * 16 + c16) * 4));
+      const float ze = half_bits_to_float(*(const uint16_t*)(from + GPW * 1024 + 256 + (u * 16 + c16) * 4));
+      const float s_ = gw + u < G ? sc : 0.0f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc[e] = __builtin_fmaf(s_, __builtin_fmaf(-(16.0f + ze), sx[u][e], p[e]), acc[e]);
+    }
+    if (i + RING < items) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");    // the slot has been read
+      fetch(in, slot);
+      advance(in);
+    }
+    slot = slot + 1 == RING ? 0 : slot + 1;
+    if (waves > 1) {
+      red[(buf * waves + wave) * 64 + lane] = acc;
       __syncthreads();
     }
-    // tile t of the batch is finished by wave t (mod waves); a lane holds rows 4q + i of column n
-    for (int t = wave; t < T; t += waves) {
-      f32x4 sum;
+    // tile tb of a batch is finished by wave tb (mod waves), in every chunk. The other buffer of partials takes
+    // the next item meanwhile: its last readers have passed the barrier above.
+    if (tb % waves == wave) {
       if (waves > 1) {
-        sum = red[t * 64 + lane];
-        for (int w = 1; w < waves; ++w) sum += red[(w * T + t) * 64 + lane];
-      } else {
-        sum = acc[0];
-#pragma unroll
-        for (int k = 1; k < T; ++k)
-          if (t == k) sum = acc[k];
+        acc = red[buf * waves * 64 + lane];
+        for (int w = 1; w < waves; ++w) acc += red[(buf * waves + w) * 64 + lane];
       }
-      const int n = (batch * T + t) * 16 + c16;
-      if (n < a.N) {
-        const float b = a.bias ? load_bias(a.bias, a.bias_dtype, n) : 0.0f;
+      if (at.chunk) acc += run[tb * 64 + lane];
+      if (at.chunk + 1 < chunks) {
+        run[tb * 64 + lane] = acc;
+      } else {
+        const int n = (blockIdx.x + at.tile * nb) * 16 + c16;   // a lane holds rows 4q + e of column n
+        if (n < a.N) {
+          const float b = a.bias ? bias[(((at.first / BATCH) & 1) * BATCH + tb) * 16 + c16] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (4 * q + i < a.M) store_out(a.Y, a.ldy, a.y_dtype, 4 * q + i, n, finish(sum[i], b, a.act));
+          for (int e = 0; e < 4; ++e)
+            if (4 * q + e < a.M) store_out(a.Y, a.ldy, a.y_dtype, 4 * q + e, n, finish(acc[e], b, a.act));
+        }
       }
     }
-    if (waves > 1 && batch + (int)gridDim.x < batches) __syncthreads();
+    buf ^= 1;
+    advance(at);
   }
 }
 
 namespace {
 
-template <bool BF16, int GPW, int T>
-void run(const GemmArgs& a, int waves, int blocks, hipStream_t st) {
-  gemv_int4_kernel<BF16, GPW, T><<<dim3(blocks), dim3(64 * waves), (size_t)waves * T * 1024, st>>>(a);
+template <bool BF16, int GPW>
+void run(const GemmArgs& a, int num_cu, hipStream_t st) {
+  const int G = a.K / 128, tiles = (a.N + 15) / 16;
+  const int chunks = (G + GPW * gemv::MAXWAVES - 1) / (GPW * gemv::MAXWAVES);
+  const int waves = (G + GPW * chunks - 1) / (GPW * chunks);
+  const size_t lds = gemv::lds_bytes(GPW, waves, chunks);
+  const int per_cu = max(1, min(gemv::CU_WAVES / waves, (int)(160 * 1024 / lds)));
+  gemv_int4_kernel<BF16, GPW><<<dim3(min(tiles, per_cu * num_cu)), dim3(64 * waves), lds, st>>>(a, chunks);
 }
 
+// Groups a wave: more waves hide more latency, fewer leave less to add. At
+// 131072 x 2560 (20 groups), M = 2, 1 / 2 / 3 / 4 groups a wave took 64 / 45 /
+// 41 / 54 us, at 19456 x 2560, M = 16, 14.9 / 13.4 / 14.2 / 16.9; short K takes
+// fewer so that a workgroup has waves at all.
 template <bool BF16>
 void dispatch(const GemmArgs& a, int num_cu, hipStream_t st) {
-  const int G = a.K / 128, tiles = (a.N + 15) / 16;
-  const int waves = min(gemv::MAXWAVES, (G + 1) / 2);
-  const int t = tiles <= 2 * num_cu ? 1 : 2;
-  const int blocks = min((tiles + t - 1) / t, 2 * num_cu);
-  if (t == 1) run<BF16, 2, 1>(a, waves, blocks, st);
-  else run<BF16, 2, 2>(a, waves, blocks, st);
+  const int G = a.K / 128;
+  if (G <= 4) run<BF16, 1>(a, num_cu, st);
+  else if (G <= 12) run<BF16, 2>(a, num_cu, st);
+  else run<BF16, 3>(a, num_cu, st);
 }
 
 }  // namespace
