@@ -15,98 +15,87 @@ namespace lowbit {
 
 namespace {
 
-constexpr int APPEND_THREADS = 256;
+constexpr int MAX_THREADS = 1024;
 // scales below this are kept as 0 (1 / s must stay finite); their values are
 // below 2^-93 and become 0
 constexpr float MIN_SCALE = 7.888609052210118e-31f;   // 2^-100
 
+// 8 consecutive values, 16-byte aligned
 template <int DT>
-__device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if constexpr (DT == DT_F16) return half_bits_to_float(((const uint16_t*)p)[i]);
-  if constexpr (DT == DT_BF16) return bf16_bits_to_float(((const uint16_t*)p)[i]);
-  return ((const float*)p)[i];
-}
-
-// N consecutive values (16-byte aligned in memory for N = 16 and for FP32; 8 bytes for N = 4 of 16 bits)
-template <int DT, int N>
-__device__ __forceinline__ void load_row(const void* p, int64_t i, float* r) {
+__device__ __forceinline__ void load8(const void* p, int64_t i, float* r) {
   if constexpr (DT == DT_F32) {
 #pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
+    for (int j = 0; j < 2; ++j) {
       const f32x4 w = *(const f32x4*)((const float*)p + i + 4 * j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) r[4 * j + e] = w[e];
     }
   } else {
+    const u32x4 w = *(const u32x4*)((const uint16_t*)p + i);
 #pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-      const u32x2 w = *(const u32x2*)((const uint16_t*)p + i + 4 * j);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-        r[4 * j + e] = DT == DT_F16 ? half_bits_to_float(h) : bf16_bits_to_float(h);
-      }
+    for (int e = 0; e < 8; ++e) {
+      const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      r[e] = DT == DT_F16 ? half_bits_to_float(h) : bf16_bits_to_float(h);
     }
   }
 }
 
-template <int DT, int N>
-__device__ __forceinline__ void store_row(void* p, int64_t i, const float* r) {
+template <int DT>
+__device__ __forceinline__ void store8(void* p, int64_t i, const float* r) {
   if constexpr (DT == DT_F32) {
 #pragma unroll
-    for (int j = 0; j < N / 4; ++j)
+    for (int j = 0; j < 2; ++j)
       *(f32x4*)((float*)p + i + 4 * j) = f32x4{r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]};
   } else {
+    u32x4 w;
 #pragma unroll
-    for (int j = 0; j < N / 4; ++j) {
-      u32x2 w;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = r[4 * j + 2 * e], y = r[4 * j + 2 * e + 1];
-        w[e] = DT == DT_F16 ? (uint32_t)float_to_half_bits(x) | (uint32_t)float_to_half_bits(y) << 16
-                            : (uint32_t)float_to_bf16_bits(x) | (uint32_t)float_to_bf16_bits(y) << 16;
-      }
-      *(u32x2*)((uint16_t*)p + i + 4 * j) = w;
-    }
+    for (int e = 0; e < 4; ++e)
+      w[e] = DT == DT_F16 ? (uint32_t)float_to_half_bits(r[2 * e]) | (uint32_t)float_to_half_bits(r[2 * e + 1]) << 16
+                          : (uint32_t)float_to_bf16_bits(r[2 * e]) | (uint32_t)float_to_bf16_bits(r[2 * e + 1]) << 16;
+    *(u32x4*)((uint16_t*)p + i) = w;
   }
 }
 
-// Unit u of a row is 32 values in two pieces of 16, placed so that a rotated
-// pair never leaves a unit: with halves apart ("x, y" = d, d + rot / 2) the
-// pieces are 16 u and rot / 2 + 16 u, with neighbours paired (and past the
-// rotated part) they are 32 u and 32 u + 16.
+// Unit u of a row is 16 values in two pieces of 8, placed so that a rotated
+// pair never leaves a unit: with halves apart (d, d + rot / 2) the pieces are
+// 8 u and rot / 2 + 8 u, with neighbours paired (and past the rotated part)
+// they are 16 u and 16 u + 8. Every piece is one 16-byte load of 16-bit
+// values, and neighbouring lanes take neighbouring pieces.
 __device__ __forceinline__ void unit_places(int u, int rot, int inter, int* d0, int* d1) {
-  if (!inter && 32 * u < rot) {
-    *d0 = 16 * u;
-    *d1 = rot / 2 + 16 * u;
+  if (!inter && 16 * u < rot) {
+    *d0 = 8 * u;
+    *d1 = rot / 2 + 8 * u;
   } else {
-    *d0 = 32 * u;
-    *d1 = 32 * u + 16;
+    *d0 = 16 * u;
+    *d1 = 16 * u + 8;
   }
 }
 
-// Rotate one unit: a holds the values of its first piece, b of its second.
-__device__ __forceinline__ void rotate_unit(float* a, float* b, int u, const KvAppendArgs& g, int64_t pos) {
-  if (32 * u >= g.rot) return;
-  const float* c = g.cos + pos * (g.rot / 2) + 16 * u;
-  const float* s = g.sin + pos * (g.rot / 2) + 16 * u;
-  float cc[16], ss[16];
-  load_row<DT_F32, 16>(c, 0, cc);
-  load_row<DT_F32, 16>(s, 0, ss);
-  if (g.inter) {
+struct Turn {             // cos and sin of a unit's eight pairs; none past the rotated part
+  float c[8], s[8];
+  bool on;
+};
+__device__ __forceinline__ void load_turn(const KvAppendArgs& g, int u, int64_t pos, Turn* t) {
+  t->on = 16 * u < g.rot;
+  if (!t->on) return;
+  load8<DT_F32>(g.cos, pos * (g.rot / 2) + 8 * u, t->c);
+  load8<DT_F32>(g.sin, pos * (g.rot / 2) + 8 * u, t->s);
+}
+
+// Rotate one unit in place: r[0 .. 7] is its first piece, r[8 .. 15] its second.
+__device__ __forceinline__ void rotate_unit(float* r, const Turn& t, int inter) {
+  if (!t.on) return;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float* p = i < 8 ? a + 2 * i : b + 2 * i - 16;
-      const float x = p[0], y = p[1];
-      p[0] = __builtin_fmaf(x, cc[i], -(y * ss[i]));
-      p[1] = __builtin_fmaf(x, ss[i], y * cc[i]);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = __builtin_fmaf(x, cc[i], -(y * ss[i]));
-      b[i] = __builtin_fmaf(x, ss[i], y * cc[i]);
+  for (int i = 0; i < 8; ++i) {
+    const int a = i, b = i + 8;
+    if (!inter) {
+      const float x = r[a], y = r[b];
+      r[a] = __builtin_fmaf(x, t.c[i], -(y * t.s[i]));
+      r[b] = __builtin_fmaf(x, t.s[i], y * t.c[i]);
+    } else {
+      const float x = r[2 * i], y = r[2 * i + 1];
+      r[2 * i] = __builtin_fmaf(x, t.c[i], -(y * t.s[i]));
+      r[2 * i + 1] = __builtin_fmaf(x, t.s[i], y * t.c[i]);
     }
   }
 }
@@ -133,8 +122,7 @@ __device__ __forceinline__ float block_max(float x, float* lds) {
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
   __syncthreads();
   float m = lds[0];
-#pragma unroll
-  for (int i = 1; i < APPEND_THREADS / 64; ++i) m = fmaxf(m, lds[i]);
+  for (int i = 1; i < (int)blockDim.x / 64; ++i) m = fmaxf(m, lds[i]);
   return m;
 }
 
@@ -147,58 +135,77 @@ __device__ __forceinline__ void new_scale(float top, float old, float* s, float*
   *ratio = old * *inv;
 }
 
+__device__ __forceinline__ uint32_t codes4(const float* r, float inv) {
+  return code(r[0], inv) | code(r[1], inv) << 8 | code(r[2], inv) << 16 | code(r[3], inv) << 24;
+}
+
+// Both writers read their new values once: the first KEEP units of a thread
+// (all of them for blocks of 64 tokens of 128) stay in registers between the
+// maximum and the codes; larger blocks read the rest again.
 template <int DT>
 __device__ void append_keys(const KvAppendArgs& g, int64_t row0, int64_t pos0, int p0, int n, int64_t id, int h,
                             float* lds, int* bad) {
-  const int D = g.c.D, U = D / 32;
+  constexpr int KEEP = 2;
+  const int D = g.c.D, U = D / 16;                           // a power of two
   uint8_t* block = g.c.k + (id * g.c.heads + h) * (int64_t)g.c.page * D;
   float* sp = g.c.ks + id * g.c.heads + h;
   const float old = p0 ? *sp : 0.0f;
-  float a[16], b[16], top = 0.0f;
-  auto fetch = [&](int i) {                                  // unit i of the new rows, rotated; non-finite values are 0
-    const int t = i / U, u = i - t * U;
+  const int shift = 31 - __builtin_clz(U);
+  // unit i of the new rows, rotated; non-finite values are 0
+  auto fetch = [&](int i, float* r) __attribute__((always_inline)) {
+    const int t = i >> shift, u = i & (U - 1);
     int d0, d1;
     unit_places(u, g.rot, g.inter, &d0, &d1);
     const int64_t at = (row0 + t) * g.k.ts + h * g.k.hs;
-    load_row<DT, 16>(g.k.p, at + d0, a);
-    load_row<DT, 16>(g.k.p, at + d1, b);
-    rotate_unit(a, b, u, g, pos0 + t);
+    load8<DT>(g.k.p, at + d0, r);
+    load8<DT>(g.k.p, at + d1, r + 8);
+    Turn turn;
+    load_turn(g, u, pos0 + t, &turn);
+    rotate_unit(r, turn, g.inter);
     int count = 0;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      if (!finite(a[e])) a[e] = 0.0f, ++count;
-      if (!finite(b[e])) b[e] = 0.0f, ++count;
-    }
+    for (int e = 0; e < 16; ++e)
+      if (!finite(r[e])) r[e] = 0.0f, ++count;
     return count;
   };
-  for (int i = threadIdx.x; i < n * U; i += APPEND_THREADS) {
-    *bad += fetch(i);
+  auto store = [&](int i, const float* r, float inv) __attribute__((always_inline)) {
+    const int t = i >> shift, u = i & (U - 1);
+    int d0, d1;
+    unit_places(u, g.rot, g.inter, &d0, &d1);
+    *(u32x2*)(block + k_byte(p0 + t, d0, D)) = u32x2{codes4(r, inv), codes4(r + 4, inv)};
+    *(u32x2*)(block + k_byte(p0 + t, d1, D)) = u32x2{codes4(r + 8, inv), codes4(r + 12, inv)};
+  };
+  float kept[KEEP][16], top = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) top = fmaxf(top, fmaxf(fabsf(a[e]), fabsf(b[e])));
+  for (int k = 0; k < KEEP; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    if (i < n * U) {
+      *bad += fetch(i, kept[k]);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(kept[k][e]));
+    }
+  }
+  for (int i = threadIdx.x + KEEP * blockDim.x; i < n * U; i += blockDim.x) {
+    float r[16];
+    *bad += fetch(i, r);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) top = fmaxf(top, fabsf(r[e]));
   }
   float s, inv, ratio;
   new_scale(block_max(top, lds), old, &s, &inv, &ratio);
-  for (int i = threadIdx.x; i < n * U; i += APPEND_THREADS) {
-    fetch(i);
-    const int t = i / U, u = i - t * U;
-    int d0, d1;
-    unit_places(u, g.rot, g.inter, &d0, &d1);
-    u32x4 x, y;
 #pragma unroll
-    for (int w = 0; w < 4; ++w) {
-      x[w] = y[w] = 0;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[w] |= code(a[4 * w + e], inv) << (8 * e);
-        y[w] |= code(b[4 * w + e], inv) << (8 * e);
-      }
-    }
-    *(u32x4*)(block + k_byte(p0 + t, d0, D)) = x;
-    *(u32x4*)(block + k_byte(p0 + t, d1, D)) = y;
+  for (int k = 0; k < KEEP; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    if (i < n * U) store(i, kept[k], inv);
+  }
+  for (int i = threadIdx.x + KEEP * blockDim.x; i < n * U; i += blockDim.x) {
+    float r[16];
+    fetch(i, r);
+    store(i, r, inv);
   }
   if (p0 && s != old) {
-    for (int i = threadIdx.x; i < p0 * (D / 16); i += APPEND_THREADS) {
-      u32x4* p = (u32x4*)(block + k_byte(i / (D / 16), i % (D / 16) * 16, D));
+    for (int i = threadIdx.x; i < p0 * U; i += blockDim.x) {
+      u32x4* p = (u32x4*)(block + k_byte(i >> shift, (i & (U - 1)) * 16, D));
       u32x4 w = *p;
 #pragma unroll
       for (int e = 0; e < 4; ++e) w[e] = rescale4(w[e], ratio);
@@ -208,80 +215,133 @@ __device__ void append_keys(const KvAppendArgs& g, int64_t row0, int64_t pos0, i
   if (threadIdx.x == 0) *sp = s;
 }
 
+// A unit here is four tokens (a quad of the block) by 8 dimensions.
 template <int DT>
 __device__ void append_values(const KvAppendArgs& g, int64_t row0, int p0, int n, int64_t id, int h, float* lds,
                               int* bad) {
-  const int D = g.c.D, F = D / 4;
+  constexpr int KEEP = 1;
+  const int D = g.c.D, F = D / 8;                            // a power of two
   uint8_t* block = g.c.v + (id * g.c.heads + h) * (int64_t)g.c.page * D;
   float* sp = g.c.vs + id * g.c.heads + h;
   const float old = p0 ? *sp : 0.0f;
-  float top = 0.0f;
-  for (int i = threadIdx.x; i < n * F; i += APPEND_THREADS) {
-    const int t = i / F, f = i - t * F;
-    float r[4];
-    load_row<DT, 4>(g.v.p, (row0 + t) * g.v.ts + h * g.v.hs + 4 * f, r);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (finite(r[e])) top = fmaxf(top, fabsf(r[e]));
-      else ++*bad;
-    }
-  }
-  float s, inv, ratio;
-  new_scale(block_max(top, lds), old, &s, &inv, &ratio);
-  // quads of tokens that hold new ones (and, after a growth, all older ones)
-  const int q0 = s != old ? 0 : p0 >> 2, q1 = (p0 + n + 3) >> 2;
-  for (int i = threadIdx.x; i < (q1 - q0) * F; i += APPEND_THREADS) {
-    const int qd = q0 + i / F, f = i % F;
-    u32x4* p = (u32x4*)(block + v_byte(4 * qd, 4 * f, D));
-    u32x4 w = {0u, 0u, 0u, 0u};
-    if (4 * qd < p0 || 4 * qd + 4 > p0 + n) {
-      w = *p;                                                // four tokens a word: older and later ones stay
-      if (s != old && 4 * qd < p0) {
-        const int keep = min(4, p0 - 4 * qd);                // tokens that follow the scale
-        const uint32_t mask = keep == 4 ? 0xFFFFFFFFu : (1u << (8 * keep)) - 1u;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = (rescale4(w[e], ratio) & mask) | (w[e] & ~mask);
-      }
-    }
+  const int shift = 31 - __builtin_clz(F);
+  const int q0 = p0 >> 2, q1 = (p0 + n + 3) >> 2, units = (q1 - q0) << shift;
+  // the new values of unit i, 0 elsewhere and where not finite
+  auto fetch = [&](int i, float (*r)[8]) __attribute__((always_inline)) {
+    const int qd = q0 + (i >> shift), f = i & (F - 1);
+    int count = 0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int t = 4 * qd + j - p0;
       if (t >= 0 && t < n) {
-        float r[4];
-        load_row<DT, 4>(g.v.p, (row0 + t) * g.v.ts + h * g.v.hs + 4 * f, r);
+        load8<DT>(g.v.p, (row0 + t) * g.v.ts + h * g.v.hs + 8 * f, r[j]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          w[e] = (w[e] & ~(255u << (8 * j))) | code(finite(r[e]) ? r[e] : 0.0f, inv) << (8 * j);
+        for (int e = 0; e < 8; ++e)
+          if (!finite(r[j][e])) r[j][e] = 0.0f, ++count;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r[j][e] = 0.0f;
       }
     }
-    *p = w;
+    return count;
+  };
+  float s, inv, ratio;
+  auto store = [&](int i, float (*r)[8]) __attribute__((always_inline)) {
+    const int qd = q0 + (i >> shift), f = i & (F - 1);
+    const int first = p0 - 4 * qd, last = p0 + n - 4 * qd;   // new tokens first .. last - 1 of the quad
+    const uint32_t older = first > 0 ? (1u << (8 * first)) - 1u : 0u;
+    const uint32_t later = last < 4 ? ~((1u << (8 * last)) - 1u) : 0u;
+    u32x4* p = (u32x4*)(block + v_byte(4 * qd, 8 * f, D));
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      u32x4 w;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int d = 4 * half + e;
+        w[e] = code(r[0][d], inv) | code(r[1][d], inv) << 8 | code(r[2][d], inv) << 16 | code(r[3][d], inv) << 24;
+      }
+      if (older | later) {                                   // other tokens of the quad stay, older ones in the new scale
+        const u32x4 was = p[half];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          w[e] = (w[e] & ~(older | later)) | ((s != old ? rescale4(was[e], ratio) : was[e]) & older) | (was[e] & later);
+      }
+      p[half] = w;
+    }
+  };
+  float kept[KEEP][4][8], top = 0.0f;
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    if (i < units) {
+      *bad += fetch(i, kept[k]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(kept[k][j][e]));
+    }
+  }
+  for (int i = threadIdx.x + KEEP * blockDim.x; i < units; i += blockDim.x) {
+    float r[4][8];
+    *bad += fetch(i, r);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(r[j][e]));
+  }
+  new_scale(block_max(top, lds), old, &s, &inv, &ratio);
+#pragma unroll
+  for (int k = 0; k < KEEP; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    if (i < units) store(i, kept[k]);
+  }
+  for (int i = threadIdx.x + KEEP * blockDim.x; i < units; i += blockDim.x) {
+    float r[4][8];
+    fetch(i, r);
+    store(i, r);
+  }
+  if (s != old) {                                            // quads of older tokens alone
+    for (int i = threadIdx.x; i < q0 * (D / 4); i += blockDim.x) {
+      u32x4* p = (u32x4*)block + i;
+      u32x4 w = *p;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = rescale4(w[e], ratio);
+      *p = w;
+    }
   }
   if (threadIdx.x == 0) *sp = s;
 }
 
-// Rotate the queries of n tokens (q heads first .. last - 1).
+// Rotate the queries of n tokens (heads first .. last - 1). A thread takes one
+// unit of one token and walks the heads with its cos and sin in registers;
+// with few tokens the heads are spread over threads too.
 template <int DT>
 __device__ void rotate_queries(const KvAppendArgs& g, int64_t row0, int64_t pos0, int n, int first, int last) {
-  const int U = g.c.D / 32, per = (last - first) * U;
-  for (int i = threadIdx.x; i < n * per; i += APPEND_THREADS) {
-    const int t = i / per, j = i - t * per, h = first + j / U, u = j % U;
+  const int U = g.c.D / 16, shift = 31 - __builtin_clz(U), units = n << shift;
+  const int ways = max(1, min(last - first, (int)blockDim.x / units));
+  for (int i = threadIdx.x; i < units * ways; i += blockDim.x) {
+    const int way = i / units, j = i - way * units, t = j >> shift, u = j & (U - 1);
     int d0, d1;
     unit_places(u, g.rot, g.inter, &d0, &d1);
-    float a[16], b[16];
-    const int64_t at = (row0 + t) * g.q.ts + h * g.q.hs, to = (row0 + t) * g.qo.ts + h * g.qo.hs;
-    load_row<DT, 16>(g.q.p, at + d0, a);
-    load_row<DT, 16>(g.q.p, at + d1, b);
-    rotate_unit(a, b, u, g, pos0 + t);
-    store_row<DT, 16>(g.qo.p, to + d0, a);
-    store_row<DT, 16>(g.qo.p, to + d1, b);
+    Turn turn;
+    load_turn(g, u, pos0 + t, &turn);
+    const int64_t at = (row0 + t) * g.q.ts, to = (row0 + t) * g.qo.ts;
+    for (int h = first + way; h < last; h += ways) {
+      float r[16];
+      load8<DT>(g.q.p, at + h * g.q.hs + d0, r);
+      load8<DT>(g.q.p, at + h * g.q.hs + d1, r + 8);
+      rotate_unit(r, turn, g.inter);
+      store8<DT>(g.qo.p, to + h * g.qo.hs + d0, r);
+      store8<DT>(g.qo.p, to + h * g.qo.hs + d1, r + 8);
+    }
   }
 }
 
 // grid: x = pages that a sequence's new tokens may touch, y = key heads,
 // value heads, then groups of query heads, z = sequences
 template <int DT>
-__global__ __launch_bounds__(APPEND_THREADS) void append_kernel(KvAppendArgs g, int q_group) {
-  __shared__ float lds[APPEND_THREADS / 64];
+__global__ __launch_bounds__(MAX_THREADS) void append_kernel(KvAppendArgs g, int q_group) {
+  __shared__ float lds[MAX_THREADS / 64];
   const int b = blockIdx.z, H = g.c.heads, page = g.c.page;
   int64_t row0;
   int n;
@@ -326,7 +386,7 @@ __device__ __forceinline__ float value_of(float s, uint32_t u) {
 
 // Dense rows of a range of the cache. grid as above: y = key heads, value heads
 template <int DT>
-__global__ __launch_bounds__(APPEND_THREADS) void read_kernel(KvReadArgs g) {
+__global__ __launch_bounds__(MAX_THREADS) void read_kernel(KvReadArgs g) {
   const int b = blockIdx.z, H = g.c.heads, page = g.c.page, D = g.c.D;
   int64_t row0;
   int n;
@@ -346,28 +406,32 @@ __global__ __launch_bounds__(APPEND_THREADS) void read_kernel(KvReadArgs g) {
   const uint8_t* block = (values ? g.c.v : g.c.k) + blk * (int64_t)page * D;
   const float s = there ? (values ? g.c.vs : g.c.ks)[blk] : 0.0f;   // no page: zeros
   if (!values) {
-    const int C = D / 16;
-    for (int i = threadIdx.x; i < n * C; i += APPEND_THREADS) {
-      const int t = i / C, d = i % C * 16;
-      const u32x4 w = *(const u32x4*)(block + k_byte(p0 + t, d, D));
-      float r[16];
+    const int C = D / 8, shift = 31 - __builtin_clz(C);
+    for (int i = threadIdx.x; i < n * C; i += blockDim.x) {
+      const int t = i >> shift, d = (i & (C - 1)) * 8;
+      const u32x2 w = *(const u32x2*)(block + k_byte(p0 + t, d, D));
+      float r[8];
 #pragma unroll
-      for (int e = 0; e < 16; ++e) r[e] = value_of(s, (w[e >> 2] >> (8 * (e & 3))) & 255u);
-      store_row<DT, 16>(g.k.p, (row0 + t) * g.k.ts + h * g.k.hs + d, r);
+      for (int e = 0; e < 8; ++e) r[e] = value_of(s, (w[e >> 2] >> (8 * (e & 3))) & 255u);
+      store8<DT>(g.k.p, (row0 + t) * g.k.ts + h * g.k.hs + d, r);
     }
   } else {
-    const int F = D / 4, q0 = p0 >> 2, q1 = (p0 + n + 3) >> 2;
-    for (int i = threadIdx.x; i < (q1 - q0) * F; i += APPEND_THREADS) {
-      const int qd = q0 + i / F, d = i % F * 4;
-      const u32x4 w = *(const u32x4*)(block + v_byte(4 * qd, d, D));
+    const int F = D / 8, shift = 31 - __builtin_clz(F), q0 = p0 >> 2, q1 = (p0 + n + 3) >> 2;
+    for (int i = threadIdx.x; i < (q1 - q0) << shift; i += blockDim.x) {
+      const int qd = q0 + (i >> shift), d = (i & (F - 1)) * 8;
+      const u32x4* p = (const u32x4*)(block + v_byte(4 * qd, d, D));
+      const u32x4 w0 = p[0], w1 = p[1];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int t = 4 * qd + j - p0;
         if (t < 0 || t >= n) continue;
-        float r[4];
+        float r[8];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) r[e] = value_of(s, (w[e] >> (8 * j)) & 255u);
-        store_row<DT, 4>(g.v.p, (row0 + t) * g.v.ts + h * g.v.hs + d, r);
+        for (int e = 0; e < 4; ++e) {
+          r[e] = value_of(s, (w0[e] >> (8 * j)) & 255u);
+          r[4 + e] = value_of(s, (w1[e] >> (8 * j)) & 255u);
+        }
+        store8<DT>(g.v.p, (row0 + t) * g.v.ts + h * g.v.hs + d, r);
       }
     }
   }
@@ -378,21 +442,31 @@ int page_slots(int tokens, int page) { return (int)(((int64_t)tokens + page - 2)
 
 }  // namespace
 
+// Threads of a workgroup: one unit of 32 new values each of the two writers
+// where the launch bound allows (128 tokens of 256 with 256 threads: 95 us
+// for 3200 tokens of 4 heads with their queries, read back too, 67 with 1024).
+static int block_threads(const KvTable& t, const KvCache& c) {
+  const int64_t n = (int64_t)(t.max_tokens < c.page ? t.max_tokens : c.page) * c.D / 32;
+  return (int)(n < 128 ? 128 : n > MAX_THREADS ? MAX_THREADS : (n + 63) / 64 * 64);
+}
+
 hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st) {
   const int q_group = 8;
   const dim3 grid(page_slots(g.t.max_tokens, g.c.page), 2 * g.c.heads + (g.q.p ? (g.q_heads + q_group - 1) / q_group : 0),
                   g.t.batch);
-  if (g.dtype == DT_F16) append_kernel<DT_F16><<<grid, APPEND_THREADS, 0, st>>>(g, q_group);
-  else if (g.dtype == DT_BF16) append_kernel<DT_BF16><<<grid, APPEND_THREADS, 0, st>>>(g, q_group);
-  else append_kernel<DT_F32><<<grid, APPEND_THREADS, 0, st>>>(g, q_group);
+  const int threads = block_threads(g.t, g.c);
+  if (g.dtype == DT_F16) append_kernel<DT_F16><<<grid, threads, 0, st>>>(g, q_group);
+  else if (g.dtype == DT_BF16) append_kernel<DT_BF16><<<grid, threads, 0, st>>>(g, q_group);
+  else append_kernel<DT_F32><<<grid, threads, 0, st>>>(g, q_group);
   return hipGetLastError();
 }
 
 hipError_t launch_kv_read(const KvReadArgs& g, hipStream_t st) {
   const dim3 grid(page_slots(g.t.max_tokens, g.c.page), 2 * g.c.heads, g.t.batch);
-  if (g.dtype == DT_F16) read_kernel<DT_F16><<<grid, APPEND_THREADS, 0, st>>>(g);
-  else if (g.dtype == DT_BF16) read_kernel<DT_BF16><<<grid, APPEND_THREADS, 0, st>>>(g);
-  else read_kernel<DT_F32><<<grid, APPEND_THREADS, 0, st>>>(g);
+  const int threads = block_threads(g.t, g.c);
+  if (g.dtype == DT_F16) read_kernel<DT_F16><<<grid, threads, 0, st>>>(g);
+  else if (g.dtype == DT_BF16) read_kernel<DT_BF16><<<grid, threads, 0, st>>>(g);
+  else read_kernel<DT_F32><<<grid, threads, 0, st>>>(g);
   return hipGetLastError();
 }
 
