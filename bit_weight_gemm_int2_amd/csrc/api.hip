@@ -31,8 +31,8 @@ hipError_t launch_gemv_int4(bool x_bf16, const GemmArgs& a, int num_cu, hipStrea
 hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st);
 hipError_t launch_kv_read(const KvReadArgs& g, hipStream_t st);
 hipError_t launch_attention(const AttnArgs& a, bool few, hipStream_t st);
-bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int num_cu,
-                    int* splits, int* split_len);
+bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
+                    int num_cu, int* splits, int* split_len);
 int64_t int4_rows(int64_t M);
 size_t int4_workspace(int M, int N, int K, int num_cu, int variant);
 size_t small_workspace_bytes(int M, int N, int K, int num_cu, int variant, int count = 1);
@@ -789,7 +789,7 @@ size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t m
   int num_cu = 0, splits = 1, len = 0;
   if (current_device(&num_cu) != LOWBIT_OK) num_cu = 256;   // no gfx950 device: the MI355X's count
   lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
-                         (int)std::min(window, max_len), num_cu, &splits, &len);
+                         (int)std::min(window, max_len), (int)head_dim, num_cu, &splits, &len);
   return attention_bytes(splits, tokens, q_heads, head_dim);
 }
 
@@ -840,7 +840,7 @@ int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_tabl
   a.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
   a.max_len = (int)max_len;
   const bool few = lowbit::attention_plan(batch, (int)H, a.group, max_tokens, max_len, (int)std::min(window, max_len),
-                                          num_cu, &a.splits, &a.split_len);
+                                          (int)D, num_cu, &a.splits, &a.split_len);
   const size_t need = attention_bytes(a.splits, tokens, q_heads, D);
   if (need && (!workspace || workspace_bytes < need)) return LOWBIT_ERR_WORKSPACE;
   if (need && !aligned(workspace, 256)) return LOWBIT_ERR_ALIGN;

@@ -181,6 +181,34 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
   for (int i = 0; i < D / 16; ++i) o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   if (w.t0 < w.t1) {
+    const int last = (w.t1 - 1) & ~15;
+    u32x4 kr[2][NI], vr[2][NI];
+    auto load_k = [&](int j, int64_t at) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) kr[j][i] = *(const u32x4*)(a.c.k + at + lane * 16 + 1024 * i);
+    };
+    auto load_v = [&](int j, int64_t at) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) vr[j][i] = *(const u32x4*)(a.c.v + at + g * 4 * D + r * 16 + 256 * i);
+    };
+    // the 16-token tile at t (clamped into the part) of block blk
+    auto tile_at = [&](int t, int32_t blk) __attribute__((always_inline)) {
+      return ((int64_t)blk << shift) * D + (int64_t)(min(t, last) & (a.c.page - 1)) * D;
+    };
+    // the first step's tiles straight from the table: their loads and those of the scales are under way together
+    int t = (w.t0 & ~15) + 32 * wave;
+    if (t < w.t1) {
+      int64_t at[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int32_t id = a.t.table[(int64_t)b * a.t.width + (min(t + 16 * j, last) >> shift)];
+        at[j] = tile_at(t + 16 * j, id >= 0 && id < a.c.pages ? id * a.c.heads + h : 0);
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_k(j, at[j]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) load_v(j, at[j]);
+    }
     load_pages(a, b, h, p0, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
     // queries: lane (g, r) holds d = 16 (g + 4 i) + 8 half .. + 7 of row r
     int64_t token;
@@ -214,37 +242,6 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
     const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = a.window ? pos1 - a.window + 1 : 0;
     __syncthreads();
 
-    const int last = (w.t1 - 1) & ~15;
-    u32x4 kr[2][NI], vr[2][NI];
-    // block and place of the 16-token tile at t (clamped into the part)
-    auto place = [&](int t, int* page) {
-      t = min(t, last);
-      *page = (t >> shift) - p0;
-      return ((int64_t)pg.blk[*page] << shift) * D + (int64_t)(t & (a.c.page - 1)) * D;
-    };
-    auto load_k = [&](int t) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        int p;
-        const uint8_t* at = a.c.k + place(t + 16 * j, &p) + lane * 16;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) kr[j][i] = *(const u32x4*)(at + 1024 * i);
-      }
-    };
-    auto load_v = [&](int t) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        int p;
-        const uint8_t* at = a.c.v + place(t + 16 * j, &p) + g * 4 * D + r * 16;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) vr[j][i] = *(const u32x4*)(at + 256 * i);
-      }
-    };
-    int t = (w.t0 & ~15) + 32 * wave;
-    if (t < w.t1) {
-      load_k(t);
-      load_v(t);
-    }
     for (; t < w.t1; t += 128) {
       f32x4 s[2];
 #pragma unroll
@@ -256,7 +253,13 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
           for (int k = 0; k < 2; ++k)
             s[j] = mfma16<false>(codes8(kr[j][i][2 * k], kr[j][i][2 * k + 1]), qf[i][k], s[j]);
       }
-      if (t + 128 < w.t1) load_k(t + 128);
+      int64_t next[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) next[j] = tile_at(t + 128 + 16 * j, pg.blk[(min(t + 128 + 16 * j, last) >> shift) - p0]);
+      if (t + 128 < w.t1) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load_k(j, next[j]);
+      }
       float rv[2], mx = NEG_INF;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -302,7 +305,10 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[4 * i + x] = mfma16<false>(codes8(vr[0][i][x], vr[1][i][x]), pf, o[4 * i + x]);
-      if (t + 128 < w.t1) load_v(t + 128);
+      if (t + 128 < w.t1) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) load_v(j, next[j]);
+      }
     }
     l = sum16(l);
   }
@@ -667,18 +673,38 @@ hipError_t launch(const AttnArgs& a, bool few, hipStream_t st) {
 
 }  // namespace
 
-// Which kernel, and how many parts the context is split into: few-row calls
-// until the parts fill the GPU a few times, many-row calls until the row
-// tiles fill it once.
-bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int num_cu,
-                    int* splits, int* split_len) {
+// Which kernel, and how many parts the context is split into. Few rows: the
+// number that a rough time estimate likes best (a round of workgroups costs
+// about 3 us and, a step of 128 tokens, 1.1 us or its bytes at 5 TB/s; a join
+// 3.5 us and 0.02 a part: one sequence of 1000 tokens and 8 heads took 10.2 us whole, 9.8 in 3 parts,
+// 9.0 in 7), but at least enough parts of 1024 tokens to fill the GPU, since
+// lengths are ragged (64 sequences of up to 1000 tokens: 12.6 us whole, 16.0
+// in two parts). Many rows: until the row tiles fill the GPU twice.
+bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
+                    int num_cu, int* splits, int* split_len) {
   const int64_t rows = max_tokens * group;
   const bool few = rows <= 32;
   int64_t span = max_len;
   if (window) span = std::min(span, (int64_t)window + max_tokens + 16);
   const int64_t tiles = batch * heads * (few ? (rows + 15) / 16 : (rows + many::ROWS - 1) / many::ROWS);
-  const int64_t want = few ? 4 * num_cu : 2 * num_cu, least = few ? 256 : 1024;
-  int64_t n = std::max<int64_t>(1, std::min(want / std::max<int64_t>(tiles, 1), span / least));
+  int64_t n = 1;
+  if (few) {
+    const int64_t slots = (int64_t)num_cu * (D == 256 ? 2 : D == 128 ? 4 : 6);   // resident workgroups
+    const int64_t fill = std::min(slots / std::max<int64_t>(tiles, 1), span / 1024);
+    double best = 1e30;
+    for (int64_t k = 1; k <= 768 && (k == 1 || k * 128 <= span); k += k < 4 ? 1 : k / 3) {
+      const int64_t steps = (span + 128 * k - 1) / (128 * k), rounds = (tiles * k + slots - 1) / slots;
+      const double step = std::max(1.1, std::min(tiles * k, slots) * 256.0 * D / 5.0e6);
+      const double us = rounds * (3.0 + step * steps) + (k > 1 ? 3.5 + 0.02 * k : 0.0);
+      if (us < best) {
+        best = us;
+        n = k;
+      }
+    }
+    n = std::max(n, fill);
+  } else {
+    n = std::max<int64_t>(1, std::min((int64_t)2 * num_cu / std::max<int64_t>(tiles, 1), span / 1024));
+  }
   int64_t len = (span + n - 1) / n;
   if (few) len = std::min<int64_t>(len, FEW_SPLIT);
   len = std::max<int64_t>(128, (len + 127) / 128 * 128);
