@@ -24,6 +24,7 @@
 //  * A page whose table entry is no page, and a token that the mask hides,
 //    have t = -inf. A row that keeps nothing gives zeros (and lse = -inf).
 #include <algorithm>
+#include <type_traits>
 
 #include "kvcache.h"
 
@@ -108,14 +109,21 @@ __device__ __forceinline__ void row_place(const AttnArgs& a, const Work& w, int 
   *head = h * a.group + row % a.group;
 }
 
-// Scales of the pages p0 .. p0 + np - 1 of sequence b into LDS.
-__device__ __forceinline__ void load_pages(const AttnArgs& a, int b, int h, int p0, int np, Pages* pg) {
+// The pages p0 .. p0 + np - 1 of sequence b: their blocks into LDS, then (by
+// the same threads) the blocks' scales.
+__device__ __forceinline__ void find_pages(const AttnArgs& a, int b, int h, int p0, int np, Pages* pg) {
   for (int i = threadIdx.x; i < np; i += blockDim.x) {
     const int32_t id = a.t.table[(int64_t)b * a.t.width + p0 + i];
     const bool there = id >= 0 && id < a.c.pages;
-    const int32_t blk = there ? id * a.c.heads + h : 0;
+    pg->blk[i] = there ? id * a.c.heads + h : 0;
+    pg->lv[i] = there ? 0.0f : NEG_INF;
+  }
+}
+__device__ __forceinline__ void load_scales(const AttnArgs& a, int np, Pages* pg) {
+  for (int i = threadIdx.x; i < np; i += blockDim.x) {
+    const int32_t blk = pg->blk[i];
+    const bool there = pg->lv[i] == 0.0f;
     const float ks = a.c.ks[blk], vs = fmaxf(a.c.vs[blk], MIN_SCALE);
-    pg->blk[i] = blk;
     pg->kf[i] = there ? ks * a.scale : 0.0f;
     pg->lv[i] = there ? __builtin_amdgcn_logf(vs) : NEG_INF;
     pg->rv[i] = 1.0f / vs;
@@ -124,8 +132,7 @@ __device__ __forceinline__ void load_pages(const AttnArgs& a, int b, int h, int 
 
 // 8 values of a query as FP32
 template <bool BF16>
-__device__ __forceinline__ void load_q8(const AttnArgs& a, int64_t at, float* x) {
-  const u32x4 w = *(const u32x4*)((const uint16_t*)a.q.p + at);
+__device__ __forceinline__ void values8(u32x4 w, float* x) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
     const uint16_t v = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
@@ -153,7 +160,7 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t token, int 
 }
 
 // ---------------------------------------------------------------------------
-// Few rows (single tokens): 16 rows a workgroup, v_mfma_f32_16x16x32_f16.
+// Few rows (single tokens, drafts): 16 rows a workgroup, v_mfma_f32_16x16x32_f16.
 // Bound by reading the cache. Four waves walk 32-token steps of the part in
 // turn, each with its own running maximum, and meet in LDS at the end. A
 // wave reads its keys and values straight into registers (16 bytes a lane,
@@ -209,7 +216,8 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) load_v(j, at[j]);
     }
-    load_pages(a, b, h, p0, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
+    find_pages(a, b, h, p0, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
+    load_scales(a, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
     // queries: lane (g, r) holds d = 16 (g + 4 i) + 8 half .. + 7 of row r
     int64_t token;
     int head;
@@ -222,7 +230,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          load_q8<BF16>(a, token * a.q.ts + head * a.q.hs + 16 * (g + 4 * i) + 8 * k, x[i][k]);
+          values8<BF16>(*(const u32x4*)((const uint16_t*)a.q.p + token * a.q.ts + head * a.q.hs + 16 * (g + 4 * i) + 8 * k), x[i][k]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][k][e]));
         }
@@ -371,56 +379,78 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 // MFMA operands (16 consecutive bytes a lane both ways).
 // ---------------------------------------------------------------------------
 namespace many {
-constexpr int ROWS = 128, TOK = 64;
+constexpr int TOK = 64;
+constexpr float SLACK = 8.0f;              // powers of two that the running maximum may lag behind
 template <int D> constexpr size_t stage() { return (size_t)TOK * D * 2 * 2; }
 template <int D> constexpr size_t lds() { return 2 * stage<D>(); }
 }  // namespace many
 
-// output dimension of row i of value tile x
+// The c-th run of 16 consecutive dimensions that a lane of half hh holds, and
+// its first dimension. Value tile x has dimension 128 (x / 4) + 4 i + x % 4 in
+// its row i (4 (i % 16) + x + 2 (i / 16) for 64 dimensions), and register e of
+// a lane is row e % 4 + 8 (e / 4) + 4 hh.
 template <int D>
-__device__ __forceinline__ int many_d(int x, int i) {
-  if constexpr (D == 64) return 4 * (i & 15) + x + 2 * (i >> 4);
-  return 128 * (x >> 2) + 4 * i + (x & 3);
+__device__ __forceinline__ int many_run(const f32x16* o, int c, int hh, float* v) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k)
+    v[k] = D == 64 ? o[k & 1][(k >> 2) + 4 * c + 8 * ((k >> 1) & 1)] : o[4 * (c >> 2) + (k & 3)][4 * (c & 3) + (k >> 2)];
+  return 128 * (c >> 2) + 4 * (8 * (c & 3) + 4 * hh);
 }
 
-template <bool BF16, int D>
-__global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_many_kernel(AttnArgs a) {
-  constexpr int TOK = many::TOK, C = D / 16, F = D / 4;
-  constexpr int NK = TOK * C / 256, VP = TOK / 8 * F, NV = (VP + 255) / 256;   // 16-byte key loads; pairs of value loads
+template <bool BF16, int D, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kernel(AttnArgs a) {
+  constexpr int TOK = many::TOK, NT = 64 * W, ROWS = 32 * W;
+  constexpr float SLACK = many::SLACK;
+  // what a thread converts: NK pieces of KW words of a key, NV pieces of VW words of a pair of value quads
+  constexpr int KW = TOK * D / 16 >= NT ? 4 : 2, NK = TOK * D / 4 / KW / NT;
+  constexpr int VW = TOK * D / 32 >= NT ? 4 : TOK * D / 16 >= NT ? 2 : 1, NV = TOK * D / 8 / VW / NT;
+  static_assert(NK >= 1 && NV >= 1, "every thread has a piece");
   constexpr int KB = TOK * D * 2;                                      // bytes of keys in a stage
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Pages pg;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hh = lane >> 5, r = lane & 31;
+  // Later row tiles see more of the context: those of every sequence start
+  // first. Workgroups go to the XCDs in turn, so with 8 heads an XCD keeps one
+  // head's keys and values; the sequences rotate so that with fewer heads no
+  // XCD is left with the short ones.
+  // Workgroups go to the XCDs in turn, so with 8 heads an XCD keeps one head's
+  // keys and values. Later row tiles see more of the context: the first
+  // sequence begins with them, the next one ends with them, and so on.
   const int h = blockIdx.x % a.c.heads, split = blockIdx.x / a.c.heads, b = blockIdx.z;
+  const int tile = b & 1 ? blockIdx.y : gridDim.y - 1 - blockIdx.y;
   Work w;
-  // later row tiles see more of the context: they start first
-  if (!find_work(a, b, many::ROWS * (gridDim.y - 1 - blockIdx.y), many::ROWS, split, &w)) return;
+  if (!find_work(a, b, ROWS * tile, ROWS, split, &w)) return;
   const int shift = 31 - __builtin_clz(a.c.page);
 
   const int rr = min(32 * wave + r, w.rows - 1);
   int64_t token;
   int head;
   row_place(a, w, h, rr, &token, &head);
-  u32x4 qf[D / 16];
+  u32x4 qf[D / 16];                                                    // the queries as they are, converted below
   float qs;
   {
-    float top = 0.0f, x[8], down;
     const int64_t at = token * a.q.ts + head * a.q.hs + 8 * hh;
+#pragma unroll
+    for (int s = 0; s < D / 16; ++s) qf[s] = *(const u32x4*)((const uint16_t*)a.q.p + at + 16 * s);
+  }
+  auto convert_queries = [&]() __attribute__((always_inline)) {
+    float x[8], top = 0.0f, down;
+#pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      load_q8<BF16>(a, at + 16 * s, x);
+      values8<BF16>(qf[s], x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
     }
     row_unit(max32(top), &down, &qs);
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
-      load_q8<BF16>(a, at + 16 * s, x);
+      values8<BF16>(qf[s], x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) qf[s][e] = pack2(x[2 * e] * down, x[2 * e + 1] * down);
     }
-  }
+  };
   const int pos = w.pos(w.row0 + rr, a.group);
   const int hi = a.causal ? min(w.t1, pos + 1) : w.t1, lo = max(w.t0, a.window ? pos - a.window + 1 : 0);
   // tokens that no row of this wave masks
@@ -437,77 +467,101 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_many_kernel(Attn
 #pragma unroll
     for (int e = 0; e < 16; ++e) o[x][e] = 0.0f;
 
-  u32x4 kr[NK], vr[NV][2];
+  uint32_t kr[NK][KW], vr[NV][2][VW];
   const int tbeg = w.t0 & ~15;
   const int seg_tokens = (PAGES - 8) << shift;                         // tokens whose pages fit the LDS
   for (int seg = tbeg; seg < w.t1; seg += seg_tokens) {                // a multiple of 64 tokens
     const int send = min(w.t1, seg + seg_tokens), p0 = seg >> shift, last = (send - 1) & ~15;
-    __syncthreads();
-    load_pages(a, b, h, p0, ((send - 1) >> shift) - p0 + 1, &pg);
+    const int np = ((send - 1) >> shift) - p0 + 1;
+    if (seg != tbeg) __syncthreads();
+    find_pages(a, b, h, p0, np, &pg);
     __syncthreads();
     auto tile_at = [&](int t) {                                        // bytes of the 16-token tile at t in its array
       t = min(t, last);
       return ((int64_t)pg.blk[(t >> shift) - p0] << shift) * D + (int64_t)(t & (a.c.page - 1)) * D;
     };
-    auto fetch = [&](int t) {
-#pragma unroll
-      for (int i = 0; i < NK; ++i) {                                   // piece (16-token tile, chunk, token)
-        const int j = tid + 256 * i, sub = j / (16 * C), in = j % (16 * C);
-        kr[i] = *(const u32x4*)(a.c.k + tile_at(t + 16 * sub) + in * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {                                   // piece (step, half, 4 d): quads half and half + 2
-        const int j = tid + 256 * i, sub = j / (2 * F), half = j / F % 2, f = j % F;
-        if (VP < 256 && j >= VP) break;
-        const uint8_t* at = a.c.v + tile_at(t + 16 * sub) + half * 4 * D + f * 16;
-        vr[i][0] = *(const u32x4*)at;
-        vr[i][1] = *(const u32x4*)(at + 8 * D);
+    auto words = [](uint32_t* to, const uint8_t* from, auto n) __attribute__((always_inline)) {
+      constexpr int N = decltype(n)::value;
+      if constexpr (N == 4) {
+        const u32x4 w = *(const u32x4*)from;
+        to[0] = w[0], to[1] = w[1], to[2] = w[2], to[3] = w[3];
+      } else if constexpr (N == 2) {
+        const u32x2 w = *(const u32x2*)from;
+        to[0] = w[0], to[1] = w[1];
+      } else {
+        to[0] = *(const uint32_t*)from;
       }
     };
-    auto stage = [&](uint8_t* to) {
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {                                   // word j of the keys' 16-token tiles
+        const int j = (tid + NT * i) * KW, sub = j / (4 * D), in = j % (4 * D);
+        words(kr[i], a.c.k + tile_at(t + 16 * sub) + in * 4, std::integral_constant<int, KW>());
+      }
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {                                   // (16-token tile, half, word): quads half and half + 2
+        const int j = (tid + NT * i) * VW, sub = j / (2 * D), half = j / D % 2, d = j % D;
+        const uint8_t* at = a.c.v + tile_at(t + 16 * sub) + half * 4 * D + d * 4;
+        words(vr[i][0], at, std::integral_constant<int, VW>());
+        words(vr[i][1], at + 8 * D, std::integral_constant<int, VW>());
+      }
+    };
+    auto stage = [&](uint8_t* to) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < NK; ++i) {                                   // keys [32-token tile][d / 8][32 tokens][8 d]
-        const int j = tid + 256 * i, sub = j / (16 * C), in = j % (16 * C), c = in >> 4, tk = 16 * (sub & 1) + (in & 15);
-        uint8_t* at = to + (sub >> 1) * (32 * D * 2) + 2 * c * 512 + tk * 16;
-        *(u32x4*)at = codes8(kr[i][0], kr[i][1]);
-        *(u32x4*)(at + 512) = codes8(kr[i][2], kr[i][3]);
+        const int j = (tid + NT * i) * KW, sub = j / (4 * D), in = j % (4 * D) / 4, tk = 16 * (sub & 1) + (in & 15);
+        uint8_t* at = to + (sub >> 1) * (32 * D * 2) + (2 * (in >> 4) + j % 4 / 2) * 512 + tk * 16;
+#pragma unroll
+        for (int e = 0; e < KW / 2; ++e) *(u32x4*)(at + 512 * e) = codes8(kr[i][2 * e], kr[i][2 * e + 1]);
       }
 #pragma unroll
       for (int i = 0; i < NV; ++i) {                                   // values [16-token step][half][tile][32 rows][8 tokens]
-        const int j = tid + 256 * i, sub = j / (2 * F), half = j / F % 2, f = j % F;
-        if (VP < 256 && j >= VP) break;
+        const int j = (tid + NT * i) * VW, sub = j / (2 * D), half = j / D % 2, f = j % D / 4;
         uint8_t* at = to + KB + (sub * 2 + half) * (D * 16);
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
+        for (int e = 0; e < VW; ++e) {
+          const int y = j % 4 + e;
           const int x = D == 64 ? (y & 1) : 4 * (f >> 5) + y, row = D == 64 ? f + 16 * (y >> 1) : f & 31;
-          *(u32x4*)(at + (x * 32 + row) * 16) = codes8(vr[i][0][y], vr[i][1][y]);
+          *(u32x4*)(at + (x * 32 + row) * 16) = codes8(vr[i][0][e], vr[i][1][e]);
         }
       }
     };
+    // Codes are fetched two tiles ahead and converted one tile ahead, between
+    // the scores' matrix instructions; past the end the last tile repeats.
     fetch(seg);
+    load_scales(a, np, &pg);
+    if (seg == tbeg) convert_queries();
     stage(smem);
+    fetch(seg + TOK);
     __syncthreads();
     int buf = 0;
     for (int t = seg; t < send; t += TOK, buf ^= 1) {
-      const bool more = t + TOK < send;
-      if (more) fetch(t + TOK);
       const uint8_t* ks = smem + buf * many::stage<D>();
       const uint8_t* vs = ks + KB;
-      if (t < any_hi && t + TOK > any_lo) {
+      uint8_t* const to = smem + (buf ^ 1) * many::stage<D>();
+      if (t >= any_hi || t + TOK <= any_lo) {
+        stage(to);
+        fetch(t + 2 * TOK);
+      } else {
         f32x16 s[2];
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 16; ++e) s[j][e] = 0.0f;
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k)
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
             s[j] = mfma32<false>(*(const u32x4*)(ks + j * (32 * D * 2) + (2 * k + hh) * 512 + r * 16), qf[k], s[j]);
-        }
+        stage(to);
+        fetch(t + 2 * TOK);
+        // scores relative to m (to 0 before a row has seen anything)
+        const float base = m > NEG_INF ? m : 0.0f;
         float rv[4], mx = NEG_INF;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int p = (min(t + 16 * u, last) >> shift) - p0;
-          const float kf = pg.kf[p] * qs, lv = pg.lv[p];
+          const float kf = pg.kf[p] * qs, lv = pg.lv[p] - base;
           rv[u] = pg.rv[p];
 #pragma unroll
           for (int e = 8 * (u & 1); e < 8 * (u & 1) + 8; ++e) s[u >> 1][e] = __builtin_fmaf(s[u >> 1][e], kf, lv);
@@ -526,19 +580,27 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_many_kernel(Attn
 #pragma unroll
           for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[j][e]);
         mx = max32(mx);
-        if (__any(mx > m)) {
-          const float n = fmaxf(m, mx), f = n > NEG_INF ? __builtin_amdgcn_exp2f(m - n) : 1.0f;
-          m = n;
-          l *= f;
+        // m follows the maximum only when that has grown by more than 2^SLACK: probabilities up to 2^SLACK keep
+        // FP16's full precision, and the accumulators are seldom rescaled
+        const bool move = mx > (m > NEG_INF ? SLACK : NEG_INF);
+        if (__any(move)) {
+          const float by = move ? mx : 0.0f, f = __builtin_amdgcn_exp2f(-by);
+          if (move) m = base + by;
+          // nothing accumulated yet: l and o are 0 and f may be anything finite
+          const float g = fminf(f, 3.0e38f);
+          l *= g;
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) o[x] *= f;
+          for (int x = 0; x < D / 32; ++x) o[x] *= g;
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) s[j][e] -= by;
         }
-        const float base = m > NEG_INF ? m : 0.0f;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           float p[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(s[u >> 1][8 * (u & 1) + e] - base);
+          for (int e = 0; e < 8; ++e) p[e] = __builtin_amdgcn_exp2f(s[u >> 1][8 * (u & 1) + e]);
           l = __builtin_fmaf(((p[0] + p[1]) + (p[2] + p[3])) + ((p[4] + p[5]) + (p[6] + p[7])), rv[u], l);
           const u32x4 pf = {pack2(p[0], p[1]), pack2(p[2], p[3]), pack2(p[4], p[5]), pack2(p[6], p[7])};
 #pragma unroll
@@ -546,7 +608,6 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_many_kernel(Attn
             o[x] = mfma32<false>(*(const u32x4*)(vs + (u * 2 + hh) * (D * 16) + (x * 32 + r) * 16), pf, o[x]);
         }
       }
-      if (more) stage(smem + (buf ^ 1) * many::stage<D>());
       __syncthreads();
     }
   }
@@ -563,23 +624,22 @@ __global__ __launch_bounds__(256, D == 256 ? 1 : 2) void attend_many_kernel(Attn
       p[1] = l;
     }
   }
+  // a lane holds runs of 16 dimensions of its row (many_run): two 16-byte stores each
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    const int i = (e & 3) + 8 * (e >> 2) + 4 * hh;
+  for (int c = 0; c < D / 32; ++c) {
+    float v[16];
+    const int d = many_run<D>(o, c, hh, v);
 #pragma unroll
-    for (int x = 0; x < D / 32; x += (D == 64 ? 2 : 4)) {
-      const int d = many_d<D>(x, i);
-      if constexpr (D == 64) {
-        const float v0 = o[x][e] * inv, v1 = o[x + 1][e] * inv;
-        if (a.splits == 1) *(uint32_t*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) = out2<BF16>(v0, v1);
-        else *(f32x2*)(a.part + slot * D + d) = f32x2{v0, v1};
-      } else {
-        const float v0 = o[x][e] * inv, v1 = o[x + 1][e] * inv, v2 = o[x + 2][e] * inv, v3 = o[x + 3][e] * inv;
-        if (a.splits == 1)
-          *(u32x2*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) = u32x2{out2<BF16>(v0, v1), out2<BF16>(v2, v3)};
-        else
-          *(f32x4*)(a.part + slot * D + d) = f32x4{v0, v1, v2, v3};
-      }
+    for (int k = 0; k < 16; ++k) v[k] *= inv;
+    if (a.splits == 1) {
+      uint16_t* to = (uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d;
+#pragma unroll
+      for (int k = 0; k < 16; k += 8)
+        *(u32x4*)(to + k) = u32x4{out2<BF16>(v[k], v[k + 1]), out2<BF16>(v[k + 2], v[k + 3]),
+                                  out2<BF16>(v[k + 4], v[k + 5]), out2<BF16>(v[k + 6], v[k + 7])};
+    } else {
+#pragma unroll
+      for (int k = 0; k < 16; k += 4) *(f32x4*)(a.part + slot * D + d + k) = f32x4{v[k], v[k + 1], v[k + 2], v[k + 3]};
     }
   }
 }
@@ -650,22 +710,24 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a) {
   if (tid == 0) store_lse(a, token, head, m, l);
 }
 
+constexpr int FEW_ROWS = 80;
 constexpr int FEW_SPLIT = 4096;            // tokens of a part that PAGES covers at pages of 16 (plus one page of offset)
 
+template <bool BF16, int D, int W>
+void launch_many(const AttnArgs& a, int rows, hipStream_t st) {
+  attend_many_kernel<BF16, D, W><<<dim3(a.c.heads * a.splits, (rows + 32 * W - 1) / (32 * W), a.t.batch), 64 * W,
+                                   many::lds<D>(), st>>>(a);
+}
+
 template <bool BF16, int D>
-hipError_t launch(const AttnArgs& a, bool few, hipStream_t st) {
+hipError_t launch(const AttnArgs& a, int waves, hipStream_t st) {
   const int rows = a.t.max_tokens * a.group;
-  if (few) {
+  if (!waves)
     attend_few_kernel<BF16, D><<<dim3(a.splits, a.c.heads * ((rows + 15) / 16), a.t.batch), 256, 0, st>>>(a);
-  } else {
-    constexpr size_t lds = many::lds<D>();
-    if (lds > 64 * 1024) {
-      hipError_t e = hipFuncSetAttribute((const void*)attend_many_kernel<BF16, D>,
-                                         hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-      if (e != hipSuccess) return e;
-    }
-    attend_many_kernel<BF16, D><<<dim3(a.c.heads * a.splits, (rows + many::ROWS - 1) / many::ROWS, a.t.batch), 256, lds, st>>>(a);
-  }
+  else if (waves == 4)
+    launch_many<BF16, D, 4>(a, rows, st);
+  else if constexpr (D == 128)
+    launch_many<BF16, D, 8>(a, rows, st);
   if (a.splits > 1)
     attend_join_kernel<BF16, D><<<dim3((unsigned)(a.t.tokens * a.q_heads)), 256, 0, st>>>(a);
   return hipGetLastError();
@@ -673,20 +735,27 @@ hipError_t launch(const AttnArgs& a, bool few, hipStream_t st) {
 
 }  // namespace
 
-// Which kernel, and how many parts the context is split into. Few rows: the
+// Which kernel, and how many parts the context is split into. Up to 80 rows go
+// in tiles of 16, each reading the context again from the caches (16 sequences
+// of up to 6000 tokens with 40 rows: 26 us against 36 in a tile of 128 rows;
+// 68 rows, four sequences: 23 against 36). Few rows: the
 // number that a rough time estimate likes best (a round of workgroups costs
 // about 3 us and, a step of 128 tokens, 1.1 us or its bytes at 5 TB/s; a join
 // 3.5 us and 0.02 a part: one sequence of 1000 tokens and 8 heads took 10.2 us whole, 9.8 in 3 parts,
 // 9.0 in 7), but at least enough parts of 1024 tokens to fill the GPU, since
 // lengths are ragged (64 sequences of up to 1000 tokens: 12.6 us whole, 16.0
 // in two parts). Many rows: until the row tiles fill the GPU twice.
-bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
+int attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
                     int num_cu, int* splits, int* split_len) {
   const int64_t rows = max_tokens * group;
-  const bool few = rows <= 32;
+  const bool few = rows <= FEW_ROWS;
   int64_t span = max_len;
   if (window) span = std::min(span, (int64_t)window + max_tokens + 16);
-  const int64_t tiles = batch * heads * (few ? (rows + 15) / 16 : (rows + many::ROWS - 1) / many::ROWS);
+  // 256 rows a workgroup halve the conversion of codes per row (4096 queries
+  // over 20000 tokens: 1147 us against 1234) but leave one workgroup a CU: only
+  // where tiles are many and long (2000 queries over 2000 tokens: 63 against 55)
+  const int waves = few ? 0 : D == 128 && span >= 8192 && batch * heads * ((rows + 255) / 256) >= 2 * num_cu ? 8 : 4;
+  const int64_t tiles = batch * heads * (few ? (rows + 15) / 16 : (rows + 32 * waves - 1) / (32 * waves));
   int64_t n = 1;
   if (few) {
     const int64_t slots = (int64_t)num_cu * (D == 256 ? 2 : D == 128 ? 4 : 6);   // resident workgroups
@@ -703,21 +772,21 @@ bool attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int
     }
     n = std::max(n, fill);
   } else {
-    n = std::max<int64_t>(1, std::min((int64_t)2 * num_cu / std::max<int64_t>(tiles, 1), span / 1024));
+    n = std::max<int64_t>(1, std::min((int64_t)8 * num_cu / waves / std::max<int64_t>(tiles, 1), span / 1024));
   }
   int64_t len = (span + n - 1) / n;
   if (few) len = std::min<int64_t>(len, FEW_SPLIT);
   len = std::max<int64_t>(128, (len + 127) / 128 * 128);
   *split_len = (int)std::min<int64_t>(len, (int64_t)1 << 30);
   *splits = (int)std::max<int64_t>(1, (span + len - 1) / len);
-  return few;
+  return waves;
 }
 
-hipError_t launch_attention(const AttnArgs& a, bool few, hipStream_t st) {
+hipError_t launch_attention(const AttnArgs& a, int waves, hipStream_t st) {
   const bool bf = a.dtype == DT_BF16;
-  if (a.c.D == 64) return bf ? launch<true, 64>(a, few, st) : launch<false, 64>(a, few, st);
-  if (a.c.D == 128) return bf ? launch<true, 128>(a, few, st) : launch<false, 128>(a, few, st);
-  return bf ? launch<true, 256>(a, few, st) : launch<false, 256>(a, few, st);
+  if (a.c.D == 64) return bf ? launch<true, 64>(a, waves, st) : launch<false, 64>(a, waves, st);
+  if (a.c.D == 128) return bf ? launch<true, 128>(a, waves, st) : launch<false, 128>(a, waves, st);
+  return bf ? launch<true, 256>(a, waves, st) : launch<false, 256>(a, waves, st);
 }
 
 }  // namespace lowbit
