@@ -30,9 +30,9 @@ hipError_t launch_quantize(int fmt, const uint16_t* W, int64_t ldw, int64_t N, i
 hipError_t launch_gemv_int4(bool x_bf16, const GemmArgs& a, int num_cu, hipStream_t st);
 hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st);
 hipError_t launch_kv_read(const KvReadArgs& g, hipStream_t st);
-hipError_t launch_attention(const AttnArgs& a, int waves, hipStream_t st);
-int attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
-                    int num_cu, int* splits, int* split_len);
+hipError_t launch_attention(const AttnArgs& a, AttnPlan p, hipStream_t st);
+AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
+                        int num_cu);
 int64_t int4_rows(int64_t M);
 size_t int4_workspace(int M, int N, int K, int num_cu, int variant);
 size_t small_workspace_bytes(int M, int N, int K, int num_cu, int variant, int count = 1);
@@ -786,11 +786,12 @@ size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t m
   if (batch < 1 || tokens < 1 || max_tokens < 1 || max_len < 0 || kv_heads < 1 || q_heads < kv_heads || window < 0 ||
       batch > 65535 || tokens >= kMaxDim || q_heads > 65536 || max_len > ((int64_t)1 << 30))
     return 0;
-  int num_cu = 0, splits = 1, len = 0;
+  int num_cu = 0;
   if (current_device(&num_cu) != LOWBIT_OK) num_cu = 256;   // no gfx950 device: the MI355X's count
-  lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
-                         (int)std::min(window, max_len), (int)head_dim, num_cu, &splits, &len);
-  return attention_bytes(splits, tokens, q_heads, head_dim);
+  const lowbit::AttnPlan p =
+      lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
+                             (int)std::min(window, max_len), (int)head_dim, num_cu);
+  return attention_bytes(p.splits, tokens, q_heads, head_dim);
 }
 
 int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
@@ -839,13 +840,15 @@ int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_tabl
   // a window that holds every token is none for the plan; the mask takes it as it is
   a.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
   a.max_len = (int)max_len;
-  const int waves = lowbit::attention_plan(batch, (int)H, a.group, max_tokens, max_len, (int)std::min(window, max_len),
-                                          (int)D, num_cu, &a.splits, &a.split_len);
+  const lowbit::AttnPlan p = lowbit::attention_plan(batch, (int)H, a.group, max_tokens, max_len,
+                                                    (int)std::min(window, max_len), (int)D, num_cu);
+  a.splits = p.splits;
+  a.split_len = p.split_len;
   const size_t need = attention_bytes(a.splits, tokens, q_heads, D);
   if (need && (!workspace || workspace_bytes < need)) return LOWBIT_ERR_WORKSPACE;
   if (need && !aligned(workspace, 256)) return LOWBIT_ERR_ALIGN;
   a.part = (float*)workspace;
-  return lowbit::launch_attention(a, waves, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+  return lowbit::launch_attention(a, p, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
 }
 
 int32_t lowbit_gelu(const void* in, void* out, int32_t dtype, int64_t count, void* stream) {

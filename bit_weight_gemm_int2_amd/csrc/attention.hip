@@ -24,6 +24,7 @@
 //  * A page whose table entry is no page, and a token that the mask hides,
 //    have t = -inf. A row that keeps nothing gives zeros (and lse = -inf).
 #include <algorithm>
+#include <cmath>
 #include <type_traits>
 
 #include "kvcache.h"
@@ -161,18 +162,20 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t token, int 
 
 // ---------------------------------------------------------------------------
 // Few rows (single tokens, drafts): 16 rows a workgroup, v_mfma_f32_16x16x32_f16.
-// Bound by reading the cache. Four waves walk 32-token steps of the part in
-// turn, each with its own running maximum, and meet in LDS at the end. A
+// Bound by reading the cache where the GPU is full, by the conversion and the
+// waves' latency (about 40 GB/s a CU, with 4, 8 or 16 waves alike) where not.
+// Four waves walk 32-token steps of the part in turn, each with its own
+// running maximum, and meet in LDS at the end. A
 // wave reads its keys and values straight into registers (16 bytes a lane,
 // whole kilobytes a wave); the next step's loads are in flight while one is
 // computed.
 // ---------------------------------------------------------------------------
 template <bool BF16, int D>
 __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
-  constexpr int NI = D / 64, LD = D + 4;
+  constexpr int NW = 4, NI = D / 64, LD = D + 4, STEP = 32 * NW;
   __shared__ Pages pg;
-  __shared__ float ml[4][2][16];
-  __shared__ __align__(16) float os[4][16][LD];
+  __shared__ float ml[NW][2][16];
+  __shared__ __align__(16) float os[NW][16][LD];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, r = lane & 15;
@@ -250,7 +253,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
     const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = a.window ? pos1 - a.window + 1 : 0;
     __syncthreads();
 
-    for (; t < w.t1; t += 128) {
+    for (; t < w.t1; t += STEP) {
       f32x4 s[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -263,8 +266,8 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       }
       int64_t next[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) next[j] = tile_at(t + 128 + 16 * j, pg.blk[(min(t + 128 + 16 * j, last) >> shift) - p0]);
-      if (t + 128 < w.t1) {
+      for (int j = 0; j < 2; ++j) next[j] = tile_at(t + STEP + 16 * j, pg.blk[(min(t + STEP + 16 * j, last) >> shift) - p0]);
+      if (t + STEP < w.t1) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) load_k(j, next[j]);
       }
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int x = 0; x < 4; ++x) o[4 * i + x] = mfma16<false>(codes8(vr[0][i][x], vr[1][i][x]), pf, o[4 * i + x]);
-      if (t + 128 < w.t1) {
+      if (t + STEP < w.t1) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) load_v(j, next[j]);
       }
@@ -326,7 +329,9 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
     ml[wave][1][r] = l;
   }
   __syncthreads();
-  const float top = fmaxf(fmaxf(ml[0][0][r], ml[1][0][r]), fmaxf(ml[2][0][r], ml[3][0][r]));
+  float top = ml[0][0][r];
+#pragma unroll
+  for (int k = 1; k < NW; ++k) top = fmaxf(top, ml[k][0][r]);
   const float f = top > NEG_INF ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
   // lane (g, r): d = 64 i + 16 g + 4 e + x of row r
 #pragma unroll
@@ -336,37 +341,29 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       *(f32x4*)&os[wave][r][64 * i + 16 * g + 4 * e] =
           f32x4{o[4 * i][e] * f, o[4 * i + 1][e] * f, o[4 * i + 2][e] * f, o[4 * i + 3][e] * f};
   __syncthreads();
-  const int row = tid >> 4, d0 = (tid & 15) * 4;
-  if (row >= w.rows) return;
-  float mm = NEG_INF, ll = 0.0f;
+  const int64_t total = a.t.tokens * a.q_heads;
+  for (int i = tid; i < w.rows * (D / 4); i += 64 * NW) {
+    const int row = i / (D / 4), d = i % (D / 4) * 4;
+    float mm = NEG_INF, ll = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) mm = fmaxf(mm, ml[k][0][row]);
+    for (int k = 0; k < NW; ++k) mm = fmaxf(mm, ml[k][0][row]);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) ll += ml[k][1][row] * (mm > NEG_INF ? __builtin_amdgcn_exp2f(ml[k][0][row] - mm) : 1.0f);
-  int64_t token;
-  int head;
-  row_place(a, w, h, row, &token, &head);
-  const float inv = a.splits == 1 ? inverse_sum(ll) : 1.0f;
-  const int64_t total = a.t.tokens * a.q_heads, slot = split * total + token * a.q_heads + head;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int d = 64 * i + d0;
+    for (int k = 0; k < NW; ++k)
+      ll += ml[k][1][row] * (mm > NEG_INF ? __builtin_amdgcn_exp2f(ml[k][0][row] - mm) : 1.0f);
     f32x4 v = *(const f32x4*)&os[0][row][d];
 #pragma unroll
-    for (int k = 1; k < 4; ++k) v += *(const f32x4*)&os[k][row][d];
-    if (a.splits == 1)
-      *(u32x2*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) =
-          u32x2{out2<BF16>(v[0] * inv, v[1] * inv), out2<BF16>(v[2] * inv, v[3] * inv)};
-    else
-      *(f32x4*)(a.part + slot * D + d) = v;
-  }
-  if (d0 == 0) {
+    for (int k = 1; k < NW; ++k) v += *(const f32x4*)&os[k][row][d];
+    int64_t token;
+    int head;
+    row_place(a, w, h, row, &token, &head);
+    const int64_t slot = split * total + token * a.q_heads + head;
     if (a.splits == 1) {
-      store_lse(a, token, head, mm, ll);
+      v *= inverse_sum(ll);
+      *(u32x2*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) = u32x2{out2<BF16>(v[0], v[1]), out2<BF16>(v[2], v[3])};
+      if (d == 0) store_lse(a, token, head, mm, ll);
     } else {
-      float* p = a.part + a.splits * total * D + 2 * slot;
-      p[0] = mm;
-      p[1] = ll;
+      *(f32x4*)(a.part + slot * D + d) = v;
+      if (d == 0) *(f32x2*)(a.part + a.splits * total * D + 2 * slot) = f32x2{mm, ll};
     }
   }
 }
@@ -720,11 +717,11 @@ void launch_many(const AttnArgs& a, int rows, hipStream_t st) {
 }
 
 template <bool BF16, int D>
-hipError_t launch(const AttnArgs& a, int waves, hipStream_t st) {
+hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
   const int rows = a.t.max_tokens * a.group;
-  if (!waves)
+  if (p.few)
     attend_few_kernel<BF16, D><<<dim3(a.splits, a.c.heads * ((rows + 15) / 16), a.t.batch), 256, 0, st>>>(a);
-  else if (waves == 4)
+  else if (p.waves == 4)
     launch_many<BF16, D, 4>(a, rows, st);
   else if constexpr (D == 128)
     launch_many<BF16, D, 8>(a, rows, st);
@@ -735,58 +732,66 @@ hipError_t launch(const AttnArgs& a, int waves, hipStream_t st) {
 
 }  // namespace
 
-// Which kernel, and how many parts the context is split into. Up to 80 rows go
-// in tiles of 16, each reading the context again from the caches (16 sequences
-// of up to 6000 tokens with 40 rows: 26 us against 36 in a tile of 128 rows;
-// 68 rows, four sequences: 23 against 36). Few rows: the
-// number that a rough time estimate likes best (a round of workgroups costs
-// about 3 us and, a step of 128 tokens, 1.1 us or its bytes at 5 TB/s; a join
-// 3.5 us and 0.02 a part: one sequence of 1000 tokens and 8 heads took 10.2 us whole, 9.8 in 3 parts,
-// 9.0 in 7), but at least enough parts of 1024 tokens to fill the GPU, since
-// lengths are ragged (64 sequences of up to 1000 tokens: 12.6 us whole, 16.0
-// in two parts). Many rows: until the row tiles fill the GPU twice.
-int attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
-                    int num_cu, int* splits, int* split_len) {
+// Which kernel, how many waves a workgroup, and how many parts the context is
+// split into. Up to 80 rows go in tiles of 16, each reading the context again
+// from the caches (16 sequences of up to 6000 tokens with 40 rows: 26 us
+// against 36 in a tile of 128 rows; 68 rows, four sequences: 23 against 36).
+// For them the number of parts that a rough time estimate likes best: a round
+// of workgroups costs about 2 us and, a step of 128 tokens, 0.8 us or its
+// bytes at 40 GB/s a CU or, for lengths 0.6 of the longest, 5 TB/s; a join,
+// with its launch, 6 us and 0.02 a part (one sequence of 1000 tokens and 8
+// heads: 9.2 us in 7 parts against 10.2 whole on the GPU, 16.3 against 12.6
+// from Python; 8 of 2000: 13.2 in parts, 16.2 whole). But at least enough
+// parts of 1024 tokens to fill the GPU, since lengths are ragged.
+// Many rows: parts until the row tiles fill the GPU twice.
+AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
+                        int num_cu) {
   const int64_t rows = max_tokens * group;
-  const bool few = rows <= FEW_ROWS;
+  AttnPlan p{};
+  p.few = rows <= FEW_ROWS;
   int64_t span = max_len;
   if (window) span = std::min(span, (int64_t)window + max_tokens + 16);
-  // 256 rows a workgroup halve the conversion of codes per row (4096 queries
-  // over 20000 tokens: 1147 us against 1234) but leave one workgroup a CU: only
-  // where tiles are many and long (2000 queries over 2000 tokens: 63 against 55)
-  const int waves = few ? 0 : D == 128 && span >= 8192 && batch * heads * ((rows + 255) / 256) >= 2 * num_cu ? 8 : 4;
-  const int64_t tiles = batch * heads * (few ? (rows + 15) / 16 : (rows + 32 * waves - 1) / (32 * waves));
-  int64_t n = 1;
-  if (few) {
+  int64_t n = 1, len;
+  if (p.few) {
+    p.waves = 4;
+    const int64_t tiles = batch * heads * ((rows + 15) / 16);
     const int64_t slots = (int64_t)num_cu * (D == 256 ? 2 : D == 128 ? 4 : 6);   // resident workgroups
     const int64_t fill = std::min(slots / std::max<int64_t>(tiles, 1), span / 1024);
+    const int64_t least = std::max<int64_t>(1, (span + FEW_SPLIT - 1) / FEW_SPLIT);
     double best = 1e30;
-    for (int64_t k = 1; k <= 768 && (k == 1 || k * 128 <= span); k += k < 4 ? 1 : k / 3) {
+    for (int64_t k = least; k == least || (k <= 768 && k * 128 <= span); k += k < 4 ? 1 : k / 3) {
       const int64_t steps = (span + 128 * k - 1) / (128 * k), rounds = (tiles * k + slots - 1) / slots;
-      const double step = std::max(1.1, std::min(tiles * k, slots) * 256.0 * D / 5.0e6);
-      const double us = rounds * (3.0 + step * steps) + (k > 1 ? 3.5 + 0.02 * k : 0.0);
+      const double wgs = (double)std::min(tiles * k, slots), bytes = 256.0 * D;
+      const double step = std::max({0.8, std::ceil(wgs / num_cu) * bytes / 4.0e4, 0.6 * wgs * bytes / 5.0e6});
+      const double us = rounds * (2.0 + step * steps) + (k > 1 ? 6.0 + 0.02 * k : 0.0);
       if (us < best) {
         best = us;
         n = k;
       }
     }
     n = std::max(n, fill);
+    len = std::min<int64_t>((span + n - 1) / n, FEW_SPLIT);
   } else {
-    n = std::max<int64_t>(1, std::min((int64_t)8 * num_cu / waves / std::max<int64_t>(tiles, 1), span / 1024));
+    // 256 rows a workgroup halve the conversion of codes per row (4096 queries
+    // over 20000 tokens: 1147 us against 1234) but leave one workgroup a CU:
+    // only where tiles are many and long (2000 queries over 2000 tokens: 63
+    // against 55)
+    p.waves = D == 128 && span >= 8192 && batch * heads * ((rows + 255) / 256) >= 2 * num_cu ? 8 : 4;
+    const int64_t tiles = batch * heads * ((rows + 32 * p.waves - 1) / (32 * p.waves));
+    n = std::max<int64_t>(1, std::min((int64_t)8 * num_cu / p.waves / std::max<int64_t>(tiles, 1), span / 1024));
+    len = (span + n - 1) / n;
   }
-  int64_t len = (span + n - 1) / n;
-  if (few) len = std::min<int64_t>(len, FEW_SPLIT);
   len = std::max<int64_t>(128, (len + 127) / 128 * 128);
-  *split_len = (int)std::min<int64_t>(len, (int64_t)1 << 30);
-  *splits = (int)std::max<int64_t>(1, (span + len - 1) / len);
-  return waves;
+  p.split_len = (int)std::min<int64_t>(len, (int64_t)1 << 30);
+  p.splits = (int)std::max<int64_t>(1, (span + len - 1) / len);
+  return p;
 }
 
-hipError_t launch_attention(const AttnArgs& a, int waves, hipStream_t st) {
+hipError_t launch_attention(const AttnArgs& a, AttnPlan p, hipStream_t st) {
   const bool bf = a.dtype == DT_BF16;
-  if (a.c.D == 64) return bf ? launch<true, 64>(a, waves, st) : launch<false, 64>(a, waves, st);
-  if (a.c.D == 128) return bf ? launch<true, 128>(a, waves, st) : launch<false, 128>(a, waves, st);
-  return bf ? launch<true, 256>(a, waves, st) : launch<false, 256>(a, waves, st);
+  if (a.c.D == 64) return bf ? launch<true, 64>(a, p, st) : launch<false, 64>(a, p, st);
+  if (a.c.D == 128) return bf ? launch<true, 128>(a, p, st) : launch<false, 128>(a, p, st);
+  return bf ? launch<true, 256>(a, p, st) : launch<false, 256>(a, p, st);
 }
 
 }  // namespace lowbit

@@ -88,4 +88,10 @@ struct AttnArgs {
   float* part;            // splits > 1: [splits][tokens * q_heads][D], then (max, sum) [splits][tokens * q_heads]
 };
 
+struct AttnPlan {
+  bool few;               // 16-row tiles, else 32 rows a wave
+  int waves;              // of a workgroup
+  int splits, split_len;
+};
+
 }  // namespace lowbit
