@@ -553,3 +553,23 @@ def test_decoding_in_a_graph(lb):
         put_back()
         for a, b in zip(step(), eager):
             assert torch.equal(a, b)
+
+
+def test_example_decodes_like_the_definition(lb, capsys, monkeypatch):
+    """The example program on a small model: prompts of different lengths, then
+    tokens one by one; its last step against float64 (2 % a layer: four bf16
+    roundings of 2^-9 and an 8-bit cache of 1/127 steps a layer, relative to the
+    logits' norm)."""
+    banner("example: small decoder")
+    import importlib.util
+    import os
+    import sys
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "text_decode.py")
+    spec = importlib.util.spec_from_file_location("text_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    monkeypatch.setattr(sys, "argv", ["text_decode", "--layers", "2", "--hidden", "256", "--q-heads", "6", "--kv-heads", "2",
+                                      "--head-dim", "64", "--mlp", "384", "--vocab", "500", "--page", "16", "--batch", "3",
+                                      "--prompt", "37", "--tokens", "9", "--check"])
+    m.main()
+    assert "relative difference" in capsys.readouterr().out
