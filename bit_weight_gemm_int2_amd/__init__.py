@@ -466,6 +466,16 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
         return torch.empty(shape, dtype=dtype, device=like.device)
 
 
+def _dense(t: torch.Tensor, stream) -> torch.Tensor:
+    """t itself, or a contiguous copy made on the stream that reads it."""
+    if t.is_contiguous():
+        return t
+    if stream is None:
+        return t.contiguous()
+    with torch.cuda.stream(stream):
+        return t.contiguous()
+
+
 def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros: torch.Tensor,
               bias: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None, activation=None,
               out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -483,7 +493,7 @@ def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
     if unit != 1 and K > 1:
         raise ValueError("x must be 2-D float16 or bfloat16 with unit stride along K")
     N = packed.shape[0]
-    packed, scales, zeros = packed.contiguous(), scales.contiguous(), zeros.contiguous()
+    packed, scales, zeros = _dense(packed, stream), _dense(scales, stream), _dense(zeros, stream)
     if packed.dtype != torch.uint8 or packed.shape != (N, K // 2):
         raise ValueError(f"packed must be uint8 [{N}, {K // 2}] for K = {K}, got {packed.dtype} {list(packed.shape)}")
     for t, nm in ((scales, "scales"), (zeros, "zeros")):
@@ -492,7 +502,7 @@ def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
     bdt = NONE
     if bias is not None:
         _cuda(bias, "bias")
-        bias = bias.contiguous()
+        bias = _dense(bias, stream)
         if bias.numel() != N or bias.dtype not in _DT:
             raise ValueError(f"bias must hold {N} float16, bfloat16 or float32 values")
         bdt = _DT[bias.dtype]

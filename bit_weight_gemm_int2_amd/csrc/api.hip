@@ -629,8 +629,8 @@ int32_t check_cache(const lowbit_kv_cache* c, const int32_t* table, int64_t widt
     return LOWBIT_ERR_SHAPE;
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256) return LOWBIT_ERR_SHAPE;
   if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return LOWBIT_ERR_SHAPE;
-  if (width < 0 || width >= kMaxDim || batch < 1 || batch > 65535 || tokens < 0 || tokens >= kMaxDim ||
-      max_tokens < 1 || max_tokens >= ((int64_t)1 << 30))
+  if (width < 0 || width >= kMaxDim || batch < 0 || batch > 65535 || tokens < 0 || tokens >= kMaxDim ||
+      max_tokens < 0 || max_tokens >= ((int64_t)1 << 30) || (tokens && (batch < 1 || max_tokens < 1)))
     return LOWBIT_ERR_SHAPE;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
       !aligned(table, 4) || !aligned(cu, 4) || !aligned(start, 4))

@@ -209,13 +209,15 @@ void run(const GemmArgs& a, int num_cu, hipStream_t st) {
 
 // Groups a wave: more waves hide more latency, fewer leave less to add. At
 // 131072 x 2560 (20 groups), M = 2, 1 / 2 / 3 / 4 groups a wave took 64 / 45 /
-// 41 / 54 us, at 19456 x 2560, M = 16, 14.9 / 13.4 / 14.2 / 16.9; short K takes
-// fewer so that a workgroup has waves at all.
+// 41 / 54 us (three: two workgroups a CU). With few tiles a CU one workgroup of
+// two groups a wave balances better and reads the activations once: 19456 x
+// 2560, M = 16, 14.9 / 12.5 / 14.2 / 16.9. Short K takes fewer so that a
+// workgroup has waves at all.
 template <bool BF16>
 void dispatch(const GemmArgs& a, int num_cu, hipStream_t st) {
-  const int G = a.K / 128;
+  const int G = a.K / 128, tiles = (a.N + 15) / 16;
   if (G <= 4) run<BF16, 1>(a, num_cu, st);
-  else if (G <= 12) run<BF16, 2>(a, num_cu, st);
+  else if (G <= 12 || (G <= 2 * gemv::MAXWAVES && tiles <= 8 * num_cu)) run<BF16, 2>(a, num_cu, st);
   else run<BF16, 3>(a, num_cu, st);
 }
 

@@ -393,7 +393,8 @@ typedef struct {
  *   block_table  int32 [batch][table_width]; cu_tokens int32 [batch + 1],
  *                rising from 0 to `tokens`; starts int32 [batch], >= 0 (all
  *                on the device, 4-byte aligned)
- *   batch        1 .. 65535; tokens >= 0 (0: nothing is done)
+ *   batch        1 .. 65535; tokens >= 0 (0, with any batch and bound of 0 and
+ *                more: nothing is done)
  *   max_tokens   at least the most new tokens of any sequence (host bound of
  *                the launch; rows past it are not handled), >= 1
  *   k, v         [tokens][kv_heads][head_dim] of `dtype` (F16, BF16, F32)

@@ -134,6 +134,7 @@ def test_kv_append_and_read_refusals(b):
     assert call(qo=Q + 2048, ots=1536) == b.ERR_DEVICE        # the queries in place, between the keys and values
     assert call(q=None, qo=None) == b.ERR_DEVICE and call(rot=0, cos=None, sin=None) == b.ERR_DEVICE
     assert call(T=0, k=None, v=None, q=None, qo=None) == b.OK
+    assert call(T=0, k=None, v=None, q=None, qo=None, batch=0, mx=0) == b.OK
     for kw, want in ((dict(table=None), "NULL"), (dict(cu=None), "NULL"), (dict(k=None), "NULL"), (dict(qo=None), "NULL"),
                      (dict(cos=None), "NULL"), (dict(rot=0), "NULL"), (dict(dt=b.NONE), "DTYPE"), (dict(batch=0), "SHAPE"),
                      (dict(batch=70000), "SHAPE"), (dict(T=-1), "SHAPE"), (dict(mx=0), "SHAPE"), (dict(rot=48), "SHAPE"),
