@@ -461,9 +461,9 @@ def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
     current stream): taken from that stream's pool, so that no pending work
     of another stream still uses it."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape) if dtype is like.dtype else like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _dense(t: torch.Tensor, stream) -> torch.Tensor:
@@ -535,12 +535,14 @@ class KVCache:
     __slots__ = ("k", "v", "k_scale", "v_scale", "kv_heads", "page", "head_dim", "struct", "ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
-        if k.dim() != 4 or k.dtype != torch.uint8 or v.dtype != torch.uint8 or v.shape != k.shape:
+        shape = k.shape
+        if len(shape) != 4 or k.dtype != torch.uint8 or v.dtype != torch.uint8 or v.shape != shape:
             raise ValueError("k and v must be uint8 [pages, kv_heads, page, head_dim] of one shape")
-        pages, heads, page, d = k.shape
+        pages, heads, page, d = shape
         self.kv_heads, self.page, self.head_dim = heads, page, d
-        if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != (pages, heads)
-                or v_scale.shape != (pages, heads)):
+        shape = shape[:2]
+        if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != shape
+                or v_scale.shape != shape):
             raise ValueError(f"k_scale and v_scale must be float32 [{pages}, {heads}]")
         for t in (k, v, k_scale, v_scale):
             if not (t.is_cuda and t.is_contiguous()):

@@ -20,8 +20,10 @@ constexpr int MAX_THREADS = 1024;
 // below 2^-93 and become 0
 constexpr float MIN_SCALE = 7.888609052210118e-31f;   // 2^-100
 
-// 8 consecutive values, 16-byte aligned
-template <int DT>
+// 8 consecutive values, 16-byte aligned. ONCE: values that nothing reads again
+// from the caches (non-temporal, as all dense stores: 11000 tokens with their
+// queries and the read-back took 86 us through the caches, 74 past them).
+template <int DT, bool ONCE = false>
 __device__ __forceinline__ void load8(const void* p, int64_t i, float* r) {
   if constexpr (DT == DT_F32) {
 #pragma unroll
@@ -31,7 +33,8 @@ __device__ __forceinline__ void load8(const void* p, int64_t i, float* r) {
       for (int e = 0; e < 4; ++e) r[4 * j + e] = w[e];
     }
   } else {
-    const u32x4 w = *(const u32x4*)((const uint16_t*)p + i);
+    const u32x4* from = (const u32x4*)((const uint16_t*)p + i);
+    const u32x4 w = ONCE ? __builtin_nontemporal_load(from) : *from;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
@@ -45,14 +48,15 @@ __device__ __forceinline__ void store8(void* p, int64_t i, const float* r) {
   if constexpr (DT == DT_F32) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      *(f32x4*)((float*)p + i + 4 * j) = f32x4{r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]};
+      __builtin_nontemporal_store(f32x4{r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]},
+                                  (f32x4*)((float*)p + i + 4 * j));
   } else {
     u32x4 w;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
       w[e] = DT == DT_F16 ? (uint32_t)float_to_half_bits(r[2 * e]) | (uint32_t)float_to_half_bits(r[2 * e + 1]) << 16
                           : (uint32_t)float_to_bf16_bits(r[2 * e]) | (uint32_t)float_to_bf16_bits(r[2 * e + 1]) << 16;
-    *(u32x4*)((uint16_t*)p + i) = w;
+    __builtin_nontemporal_store(w, (u32x4*)((uint16_t*)p + i));
   }
 }
 
@@ -328,8 +332,8 @@ __device__ void rotate_queries(const KvAppendArgs& g, int64_t row0, int64_t pos0
     const int64_t at = (row0 + t) * g.q.ts, to = (row0 + t) * g.qo.ts;
     for (int h = first + way; h < last; h += ways) {
       float r[16];
-      load8<DT>(g.q.p, at + h * g.q.hs + d0, r);
-      load8<DT>(g.q.p, at + h * g.q.hs + d1, r + 8);
+      load8<DT, true>(g.q.p, at + h * g.q.hs + d0, r);
+      load8<DT, true>(g.q.p, at + h * g.q.hs + d1, r + 8);
       rotate_unit(r, turn, g.inter);
       store8<DT>(g.qo.p, to + h * g.qo.hs + d0, r);
       store8<DT>(g.qo.p, to + h * g.qo.hs + d1, r + 8);
@@ -451,7 +455,8 @@ static int block_threads(const KvTable& t, const KvCache& c) {
 }
 
 hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st) {
-  const int q_group = 8;
+  // two heads a workgroup: 66 us for 11000 tokens with read-back, 70 with four, 74 with eight
+  const int q_group = 2;
   const dim3 grid(page_slots(g.t.max_tokens, g.c.page), 2 * g.c.heads + (g.q.p ? (g.q_heads + q_group - 1) / q_group : 0),
                   g.t.batch);
   const int threads = block_threads(g.t, g.c);
