@@ -573,3 +573,30 @@ def test_example_decodes_like_the_definition(lb, capsys, monkeypatch):
                                       "--prompt", "37", "--tokens", "9", "--check"])
     m.main()
     assert "relative difference" in capsys.readouterr().out
+
+
+def test_attention_long_prompt_in_256_row_tiles(lb):
+    """A prompt chunk long enough for 256 rows a workgroup, over more pages than
+    one segment holds, against float64 on sampled queries (keys and values read
+    back from the cache, exact in FP32)."""
+    banner("attention: 2100 queries of 64 heads over 9000 tokens")
+    H, Hq, D, page, L, n = 8, 64, 128, 16, 9000, 2100
+    P = Paged([L], H, page, D, seed=90)
+    cache, table = P.cache(lb), _i32(P.table)
+    q, _ = _values(np.random.default_rng(91), (n, Hq, D), "bf16")
+    out = lb.attention(q, cache, table, _i32([0, n]), _i32([L]), n, L)
+    k, v = lb.kv_read(cache, table, _i32([0, L]), _i32([0]), L, L, torch.float32)
+    k, v = k.double(), v.double()
+    vs = torch.from_numpy(P.vs[P.table[0][np.arange(L) // page]]).cuda().double()
+    rows = [0, 1, 31, 32, 63, 64, 1000, 1027, 2047, 2048, 2098, 2099]
+    for i in rows:
+        for h in (0, 7, 8, 29, 63):
+            seen, g = L - n + i + 1, h // (Hq // H)
+            s = (k[:seen, g] @ q[i, h].double()) * D ** -0.5
+            e = torch.exp(s - s.max())
+            want, mag = (e @ v[:seen, g]) / e.sum(), (e @ v[:seen, g].abs()) / e.sum()
+            peak = 127 * seen * (e * vs[:seen, g]).max() / e.sum()
+            d = (out[i, h].double() - want).abs()
+            half = torch.from_numpy(np.asarray(_half_ulp(np.maximum(want.abs().cpu().numpy(), np.abs(to_host64(out[i, h]))),
+                                                         out.dtype))).cuda()
+            assert (d <= 2.0 ** -10 * mag + 2.0 ** -25 * peak + half).all(), (i, h)
