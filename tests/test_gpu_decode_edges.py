@@ -1,0 +1,112 @@
+"""The decoding operators on paths and inputs that the tests of test_gpu_decode.py
+do not reach: definitions, tolerances and helpers as there unless a test says
+otherwise."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as od
+from gpu_util import banner, to_host64
+from test_gpu_decode import Paged, _attend, _half_ulp, _i32, _values, lb  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------- the many-row kernel (over 80 rows a head) ---
+
+def _parts(lb, lens, new, H, Hq, D, window=0):
+    """Parts that the call's context is split into (1: no workspace)."""
+    T = sum(new)
+    need = lb.lib().lowbit_attention_workspace_bytes(len(lens), T, max(new), max(lens), Hq, H, D, window)
+    assert need % (T * Hq * (D + 2) * 4) == 0
+    return max(1, need // (T * Hq * (D + 2) * 4))
+
+
+MANY = [  # lens, new, H, Hq, page, D, dtype, causal, window, parts
+    ([3000], [100], 1, 1, 16, 128, "bf16", True, 0, 2),
+    ([3000, 1100], [100, 90], 1, 1, 64, 64, "f16", True, 0, 2),       # the second part of a shorter sequence is empty
+    ([6000], [100], 1, 2, 64, 64, "f16", True, 3000, 3),
+    ([4500], [100], 1, 1, 16, 256, "f16", False, 0, 4),
+    ([4500], [45], 1, 2, 128, 256, "bf16", True, 0, 4),
+    ([2200], [2200], 1, 1, 32, 64, "bf16", True, 0, 2),               # later parts that early rows do not see
+    ([2100, 40], [30, 40], 1, 3, 16, 128, "f16", True, 0, 2),
+    ([2500], [90], 1, 1, 16, 128, "bf16", False, 2300, 2),
+    ([200], [100], 1, 1, 16, 64, "f16", True, 10, 1),                 # windows of part of a tile
+    ([200], [100], 1, 1, 32, 128, "bf16", True, 3, 1),
+    ([200], [100], 1, 2, 16, 256, "bf16", True, 1, 1),
+    ([300], [90], 1, 1, 256, 128, "f16", False, 20, 1),
+    ([60], [100], 1, 2, 16, 64, "bf16", True, 0, 1),                  # queries before the first token
+    ([0, 70], [90, 70], 1, 2, 16, 128, "f16", True, 0, 1),            # nothing cached
+]
+
+
+@pytest.mark.parametrize("case", MANY, ids=[str(i) for i in range(len(MANY))])
+def test_attention_many_rows(lb, case):
+    lens, new, H, Hq, page, D, dt, causal, window, parts = case
+    banner(f"attention, many rows {case}")
+    assert max(new) * (Hq // H) > 80 and _parts(lb, lens, new, H, Hq, D, window) == parts
+    _attend(lb, lens, new, H, Hq, page, D, dt, seed=200 + len(lens) + D, causal=causal, window=window, strided=(D == 128))
+
+
+@pytest.mark.parametrize("lens,page", [((200, 100), 16), ((2500, 1200), 64)])
+def test_attention_many_rows_missing_pages_and_short_tables(lb, lens, page):
+    banner(f"attention, many rows with holes, {lens}")
+    lens, new = list(lens), [90, 90]
+    assert _parts(lb, lens, new, 2, 4, 128) == (2 if lens[0] > 2000 else 1)
+    _attend(lb, lens, new, 2, 4, page, 128, "bf16", seed=220, hole=(0, 3, -1))
+    _attend(lb, lens, new, 2, 4, page, 128, "bf16", seed=221, hole=(1, 0, 10 ** 6))
+    # a table shorter than the lengths: they count as what it holds
+    _attend(lb, lens, new, 2, 4, page, 128, "bf16", seed=223, width=lens[0] // page - 3)
+    P = Paged(lens, 2, page, 128, seed=224)                    # every page missing: zeros
+    P.table[:] = -1
+    assert (_attend(lb, lens, new, 2, 4, page, 128, "f16", kv=P) == 0).all()
+
+
+@pytest.mark.parametrize("lens,page", [((170, 133), 16), ((2500, 2133), 64)])
+def test_attention_many_rows_masked_tokens_hold_anything(lb, lens, page):
+    """As for few rows, one part and two: codes behind the length, scales of pages
+    that are not used and entries of the table behind the last page do not matter,
+    nor does what a missing page's stand-in (page 0) holds."""
+    banner(f"attention, many rows, garbage, {lens}")
+    n, H, D = 90, 1, 64
+    P = Paged(list(lens), H, page, D, seed=230, spare=6)
+    P.table[P.table == 0] = min(set(range(1, P.pages)) - set(P.table.ravel()))   # page 0 is nobody's
+    P.table[0, 1] = -1
+    q = torch.randn((2 * n, 2, D), device="cuda").half()
+    call = lambda: lb.attention(q, P.cache(lb), _i32(P.table), _i32([0, n, 2 * n]), _i32(list(lens)), n, max(lens))  # noqa: E731
+    clean = call()
+    used = [set(P.table[b, :-(-lens[b] // page)]) for b in range(2)]
+    for p in range(P.pages):
+        if p not in used[0] | used[1]:
+            P.ks[p], P.vs[p], P.k[p], P.v[p] = np.nan, np.nan, 255, 0
+    P.table[1, -(-lens[1] // page):] = -5
+    d = np.arange(D)
+    for b in range(2):
+        last = P.table[b, (lens[b] - 1) // page]
+        for t in range(lens[b] % page, page):
+            P.k[last, 0].reshape(-1)[od.k_place(t, d, D)] = 255
+            P.v[last, 0].reshape(-1)[od.v_place(t, d, D)] = 0
+    again = call()
+    assert torch.isfinite(clean).all() and torch.equal(again, clean)
+
+
+def test_attention_many_rows_several_segments_of_pages(lb):
+    """Four waves a workgroup over more pages than one segment holds (4096 tokens in
+    pages of 16), the context in one part: sampled rows against float64."""
+    banner("attention: 530 queries of 64 heads of 64 over 5000 tokens")
+    H, Hq, D, page, L, n = 8, 64, 64, 16, 5000, 530
+    assert _parts(lb, [L], [n], H, Hq, D) == 1
+    P = Paged([L], H, page, D, seed=240)
+    cache, table = P.cache(lb), _i32(P.table)
+    q, hq = _values(np.random.default_rng(241), (n, Hq, D), "f16")
+    out = lb.attention(q, cache, table, _i32([0, n]), _i32([L]), n, L)
+    k, v = (t.double().cpu().numpy() for t in lb.kv_read(cache, table, _i32([0, L]), _i32([0]), L, L, torch.float32))
+    vs = P.vs[P.table[0][np.arange(L) // page]].astype(np.float64)
+    O = to_host64(out)
+    for i in (0, 15, 16, 31, 300, 528, 529):
+        for h in (0, 8, 33, 63):
+            kv = h // (Hq // H)
+            want, _, mag, peak = od.attention(hq[i:i + 1, h:h + 1], k[:, kv:kv + 1], v[:, kv:kv + 1], vs[:, kv:kv + 1],
+                                              L - n + i, D ** -0.5, True, 0)
+            bound = 2.0 ** -10 * mag + 2.0 ** -25 * peak + _half_ulp(np.maximum(np.abs(want), np.abs(O[i, h])), out.dtype)
+            assert (np.abs(O[i, h] - want) <= bound).all(), (i, h)
