@@ -5,9 +5,11 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
+import workloads as wl
 from oracle import paged as od
-from gpu_util import banner, to_host64
-from test_gpu_decode import Paged, _attend, _half_ulp, _i32, _values, lb  # noqa: F401
+from gpu_util import TORCH_DT, banner, dev_bits, to_host64
+from test_gpu_decode import Paged, _attend, _f16, _gemv_check, _half_ulp, _i32, _values, lb  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -110,3 +112,24 @@ def test_attention_many_rows_several_segments_of_pages(lb):
                                               L - n + i, D ** -0.5, True, 0)
             bound = 2.0 ** -10 * mag + 2.0 ** -25 * peak + _half_ulp(np.maximum(np.abs(want), np.abs(O[i, h])), out.dtype)
             assert (np.abs(O[i, h] - want) <= bound).all(), (i, h)
+
+
+def test_gemv_int4_and_gemm_int4_agree(lb):
+    """The two entry points on the same operands differ by no more than both
+    contracts' bounds together (the larger kernel's adds 2^-19 (128 + max|z|) sum|x s|
+    where this one has 16)."""
+    banner("gemv int4 against gemm int4")
+    for M, dt in ((1, "bf16"), (7, "f16"), (16, "bf16")):
+        lin = wl.make_int4_linear(f"gv_gm_{M}", M, 3000, 2560, dt, seed=250 + M, with_bias=True)
+        y = to_host64(_gemv_check(lb, lin))
+        q = lb.pack_int4(torch.from_numpy(np.ascontiguousarray(lin.q)).cuda())
+        z = to_host64(lb.gemm_int4(dev_bits(lin.x, dt), q, _f16(lin.scales), _f16(lin.zeros), bias=_f16(lin.bias),
+                                   out_dtype=TORCH_DT[lin.y_dtype]))
+        A = oracle.linear_int4(lin.x, dt, lin.q, lin.scales, lin.zeros, lin.bias)
+        Mg = oracle.magnitude_int4(lin.x, dt, lin.q, lin.scales, lin.zeros, lin.bias)
+        s = np.repeat(np.abs(lin.scales.astype(np.float64)), oracle.GROUP, axis=1)
+        terms = np.abs(oracle.decode(lin.x, dt)) @ s.T
+        zmax = np.abs(lin.zeros.astype(np.float64)).max(axis=1)[None, :]
+        bound = (oracle.bound(A, Mg, lin.y_dtype, y) + oracle.bound(A, Mg, lin.y_dtype, z)
+                 + 2.0 ** -19 * (144.0 + 2 * zmax) * terms)
+        assert (np.abs(y - z) <= bound).all()
