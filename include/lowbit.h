@@ -381,8 +381,8 @@ typedef struct {
  *             new values, s_old its scale before (0 for a block whose first
  *             token is new). Scales below 2^-100 become 0.
  *   codes     128 + rint(r / scale). When a block's scale grows its older
- *             codes c = u - 128 become rint(c s_old / scale).
- * FP32 arithmetic; stored values are within 0.5001 scale + 2^-93 of the
+ *             codes c = u - 128 become rint(c (s_old / scale)).
+ * FP32 arithmetic, ties to even; stored values are within 0.5001 scale + 2^-93 of the
  * (rotated) input, and each later growth of the block adds at most half of
  * its new scale. The result is a pure function of the input. NaN and infinite
  * values (after the rotation) are stored as 0 and counted in bad_count[0];

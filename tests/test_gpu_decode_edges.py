@@ -14,6 +14,68 @@ from test_gpu_decode import Paged, _attend, _f16, _gemv_check, _half_ulp, _i32, 
 pytestmark = pytest.mark.gpu
 
 
+# ------------------------------------------------------------------ appending ---
+
+def _append_both(lb, cache, rows, start, dt):
+    t = torch.from_numpy(rows).cuda().to(TORCH_DT[dt])
+    lb.kv_append(t, t, cache, _i32([[0]]), _i32([0, len(rows)]), _i32([start]), len(rows))
+    torch.cuda.synchronize()
+
+
+def _codes_and_scale(cache, page, D):
+    return [(od.block_codes(c.cpu().numpy()[0, 0], n, page, D), np.float32(s.cpu().numpy()[0, 0]))
+            for n, c, s in (("k", cache.k, cache.k_scale), ("v", cache.v, cache.v_scale))]
+
+
+@pytest.mark.parametrize("m", [1, 3, 7, 13, 41, 61, 83])
+def test_append_ties_go_to_even(lb, m):
+    """A block whose largest magnitude is 127 m has the scale m exactly, and the
+    values (n + 1/2) m lie on ties, in FP32 as in the definition: no tolerance.
+    Older codes that follow a scale grown to 2 m or to 82 lie on ties too."""
+    banner(f"append ties, scale {m}")
+    page, D = 16, 64
+    n = np.arange(-127, 127) + 0.5
+    rows = np.zeros((8, 1, D), dtype=np.float32)
+    rows.reshape(-1)[:len(n)] = n * m
+    rows[7, 0, 63] = 127 * m
+    cache = lb.new_kv_cache(1, 1, page, D)
+    _append_both(lb, cache, rows, 0, "f32")
+    want = np.rint(rows[:, 0].astype(np.float64) / m).astype(np.int64)
+    for codes, scale in _codes_and_scale(cache, page, D):
+        assert scale == m and np.array_equal(codes[:8], want)
+    top = 2 * m if m < 41 else 82
+    if top < m:
+        return
+    _append_both(lb, cache, np.full((1, 1, D), 127 * top, dtype=np.float32), 8, "f32")
+    want = np.rint(want.astype(np.float32) * (np.float32(m) / np.float32(top))).astype(np.int64)
+    for codes, scale in _codes_and_scale(cache, page, D):
+        assert scale == max(m, top) and np.array_equal(codes[:8], want) and (codes[8] == 127).all()
+
+
+@pytest.mark.parametrize("dt", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("page,D", [(16, 64), (64, 128), (256, 256)])
+def test_append_is_the_fp32_definition_bit_for_bit(lb, page, D, dt):
+    """Without rotation: scale = a / 127, codes rint(r / scale), older codes
+    rint(c (s_old / s)), each quotient rounded once in FP32."""
+    banner(f"append against FP32 arithmetic, page {page}, D {D}, {dt}")
+    g = np.random.default_rng(page + D)
+    cache = lb.new_kv_cache(1, 1, page, D)
+    f = np.float32
+    codes, scale = np.zeros((page, D), dtype=np.int64), f(0)
+    at = 0
+    for n, size in ((page // 2 - 1, 1.0), (3, 0.5), (2, 1.7), (page // 4, 40.0)):
+        rows = (g.standard_normal((n, 1, D)) * size).astype(np.float32)
+        rows = torch.from_numpy(rows).to(TORCH_DT[dt]).float().numpy()
+        _append_both(lb, cache, rows, at, dt)
+        new = max(scale, f(np.abs(rows).max()) / f(127))
+        if at and new != scale:
+            codes[:at] = np.rint(codes[:at].astype(f) * (scale / new))
+        codes[at:at + n] = np.clip(np.rint(rows[:, 0] / new), -127, 127)
+        at, scale = at + n, new
+        for have, s in _codes_and_scale(cache, page, D):
+            assert s == scale and np.array_equal(have[:at], codes[:at])
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
