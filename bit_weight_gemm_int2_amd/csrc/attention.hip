@@ -12,11 +12,18 @@
 //    is exact and sums are FP32.
 //  * Key scales multiply the FP32 scores. Value scales go into the softmax
 //    exponent: with t_j = s_j + log2 s_v(j) (scores in powers of two) and the
-//    running maximum m of t_j, p'_j = 2^(t_j - m) is at most 1, the values'
-//    product needs no scaling per page, and sum_j p_j is the FP32 sum of
-//    p'_j / s_v(j), taken before p' is rounded to FP16 for the matrix
-//    product. One pass over the cache, with the accumulators rescaled only
-//    when a maximum grows.
+//    running maximum m of t_j, p'_j = 2^(t_j - m) needs no scaling per page in
+//    the values' product, and sum_j p_j is the FP32 sum of p'_j / s_v(j), taken
+//    before p' is rounded to FP16 for the matrix product. One pass over the
+//    cache, with the accumulators rescaled only when a maximum grows.
+//  * FP16 probabilities: each is off by at most 2^-11, independently, so the
+//    result by about 2^-12, less than a BF16 output's rounding (2^-9) and as
+//    much as an FP16 one's; FP32 ones would double the matrix instructions.
+//    They carry a factor of 2^TOP that puts the largest near the top of FP16's
+//    range, so that tokens of 2^-28 of it (2^-23 for many rows) still have full
+//    precision: where one token holds nearly all of the sum and has small
+//    values, such tokens are the result (with the largest at 1, 4000 tokens of
+//    2^-25 each beside such ones came out 32 to 48 % off).
 //  * Scores are computed transposed (keys as the MFMA's rows), which leaves
 //    every lane with probabilities of one query in just the order in which
 //    the values' product wants them: no exchange between lanes but the
@@ -42,7 +49,7 @@ constexpr float NEG_INF = -__builtin_inff();
 
 struct Pages {
   int32_t blk[PAGES];                      // page * heads + head, 0 where there is no page
-  float kf[PAGES], lv[PAGES], rv[PAGES];   // key scale * scale, log2 and reciprocal of the value scale
+  float kf[PAGES], lv[PAGES], rv[PAGES];   // key scale * scale, log2 and a unit's quotient of the value scale
 };
 
 // Two codes (bytes 0, 1 or 2, 3 of w) as FP16.
@@ -120,14 +127,14 @@ __device__ __forceinline__ void find_pages(const AttnArgs& a, int b, int h, int 
     pg->lv[i] = there ? 0.0f : NEG_INF;
   }
 }
-__device__ __forceinline__ void load_scales(const AttnArgs& a, int np, Pages* pg) {
+__device__ __forceinline__ void load_scales(const AttnArgs& a, int np, float unit, Pages* pg) {
   for (int i = threadIdx.x; i < np; i += blockDim.x) {
     const int32_t blk = pg->blk[i];
     const bool there = pg->lv[i] == 0.0f;
     const float ks = a.c.ks[blk], vs = fmaxf(a.c.vs[blk], MIN_SCALE);
     pg->kf[i] = there ? ks * a.scale : 0.0f;
     pg->lv[i] = there ? __builtin_amdgcn_logf(vs) : NEG_INF;
-    pg->rv[i] = 1.0f / vs;
+    pg->rv[i] = unit / vs;
   }
 }
 
@@ -176,6 +183,7 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t token, int 
 template <bool BF16, int D, bool ONCE>
 __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
   constexpr int NW = 4, NI = D / 64, LD = D + 4, STEP = 32 * NW;
+  constexpr float TOP = 14.0f, UNSHIFT = 0x1p-14f;                     // p' up to 2^14
   __shared__ Pages pg;
   __shared__ float ml[NW][2][16];
   __shared__ __align__(16) float os[NW][16][LD];
@@ -226,7 +234,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       for (int j = 0; j < 2; ++j) load_v(j, at[j]);
     }
     find_pages(a, b, h, p0, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
-    load_scales(a, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
+    load_scales(a, ((w.t1 - 1) >> shift) - p0 + 1, 1.0f, &pg);
     // queries: lane (g, r) holds d = 16 (g + 4 i) + 8 half .. + 7 of row r
     int64_t token;
     int head;
@@ -307,7 +315,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i] *= f;
       }
-      const float base = m > NEG_INF ? m : 0.0f;
+      const float base = (m > NEG_INF ? m : 0.0f) - TOP;
       u32x4 pf;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
@@ -327,7 +335,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
         for (int j = 0; j < 2; ++j) load_v(j, next[j]);
       }
     }
-    l = sum16(l);
+    l = sum16(l) * UNSHIFT;
   }
   // the waves meet: common maximum, then sums in wave order
   if (g == 0) {
@@ -338,7 +346,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
   float top = ml[0][0][r];
 #pragma unroll
   for (int k = 1; k < NW; ++k) top = fmaxf(top, ml[k][0][r]);
-  const float f = top > NEG_INF ? __builtin_amdgcn_exp2f(m - top) : 1.0f;
+  const float f = top > NEG_INF ? __builtin_amdgcn_exp2f(m - top) * UNSHIFT : UNSHIFT;
   // lane (g, r): d = 64 i + 16 g + 4 e + x of row r
 #pragma unroll
   for (int i = 0; i < NI; ++i)
@@ -383,7 +391,11 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 // ---------------------------------------------------------------------------
 namespace many {
 constexpr int TOK = 64;
-constexpr float SLACK = 8.0f;              // powers of two that the running maximum may lag behind
+// Powers of two that the running maximum may lag behind, and that p' is moved
+// up by: together 15, FP16's limit. Rows ruled by tokens of value 0 were off by
+// 0.0039 with 8 + 7, 0.0021 with 6 + 9, 0.0020 with 4 + 11 (0.0018 is the BF16
+// output's rounding); four prompts of 512 took 24.1, 24.4 and 24.9 us.
+constexpr float SLACK = 6.0f, TOP = 9.0f, UNSHIFT = 0x1p-9f;
 template <int D> constexpr size_t stage() { return (size_t)TOK * D * 2 * 2; }
 template <int D> constexpr size_t lds() { return 2 * stage<D>(); }
 }  // namespace many
@@ -403,7 +415,7 @@ __device__ __forceinline__ int many_run(const f32x16* o, int c, int hh, float* v
 template <bool BF16, int D, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kernel(AttnArgs a) {
   constexpr int TOK = many::TOK, NT = 64 * W, ROWS = 32 * W;
-  constexpr float SLACK = many::SLACK;
+  constexpr float SLACK = many::SLACK, TOP = many::TOP, UNSHIFT = many::UNSHIFT;
   // what a thread converts: NK pieces of KW words of a key, NV pieces of VW words of a pair of value quads
   constexpr int KW = TOK * D / 16 >= NT ? 4 : 2, NK = TOK * D / 4 / KW / NT;
   constexpr int VW = TOK * D / 32 >= NT ? 4 : TOK * D / 16 >= NT ? 2 : 1, NV = TOK * D / 8 / VW / NT;
@@ -532,7 +544,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
     // Codes are fetched two tiles ahead and converted one tile ahead, between
     // the scores' matrix instructions; past the end the last tile repeats.
     fetch(seg);
-    load_scales(a, np, &pg);
+    load_scales(a, np, UNSHIFT, &pg);                                  // the sum takes the factor off again
     if (seg == tbeg) convert_queries();
     stage(smem);
     fetch(seg + TOK);
@@ -558,13 +570,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
             s[j] = mfma32<false>(*(const u32x4*)(ks + j * (32 * D * 2) + (2 * k + hh) * 512 + r * 16), qf[k], s[j]);
         stage(to);
         fetch(t + 2 * TOK);
-        // scores relative to m (to 0 before a row has seen anything)
-        const float base = m > NEG_INF ? m : 0.0f;
+        // scores relative to m (to 0 before a row has seen anything), times 2^TOP
+        const float base = m > NEG_INF ? m : 0.0f, low = base - TOP;
         float rv[4], mx = NEG_INF;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int p = (min(t + 16 * u, last) >> shift) - p0;
-          const float kf = pg.kf[p] * qs, lv = pg.lv[p] - base;
+          const float kf = pg.kf[p] * qs, lv = pg.lv[p] - low;
           rv[u] = pg.rv[p];
 #pragma unroll
           for (int e = 8 * (u & 1); e < 8 * (u & 1) + 8; ++e) s[u >> 1][e] = __builtin_fmaf(s[u >> 1][e], kf, lv);
@@ -583,11 +595,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
 #pragma unroll
           for (int e = 0; e < 16; ++e) mx = fmaxf(mx, s[j][e]);
         mx = max32(mx);
-        // m follows the maximum only when that has grown by more than 2^SLACK: probabilities up to 2^SLACK keep
-        // FP16's full precision, and the accumulators are seldom rescaled
-        const bool move = mx > (m > NEG_INF ? SLACK : NEG_INF);
+        // m follows the maximum only when that has grown by more than 2^SLACK: FP16 holds p' up to 2^(TOP + SLACK),
+        // and the accumulators are seldom rescaled
+        const bool move = mx > (m > NEG_INF ? TOP + SLACK : NEG_INF);
         if (__any(move)) {
-          const float by = move ? mx : 0.0f, f = __builtin_amdgcn_exp2f(-by);
+          const float by = move ? mx - TOP : 0.0f, f = __builtin_amdgcn_exp2f(-by);
           if (move) m = base + by;
           // nothing accumulated yet: l and o are 0 and f may be anything finite
           const float g = fminf(f, 3.0e38f);
@@ -617,7 +629,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
   l = sum32(l);
   if (32 * wave + r >= w.rows) return;
   const int64_t total = a.t.tokens * a.q_heads, slot = split * total + token * a.q_heads + head;
-  const float inv = a.splits == 1 ? inverse_sum(l) : 1.0f;
+  const float inv = a.splits == 1 ? inverse_sum(l) * UNSHIFT : UNSHIFT;
   if (hh == 0) {
     if (a.splits == 1) {
       store_lse(a, token, head, m, l);

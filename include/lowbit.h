@@ -441,9 +441,10 @@ int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table,
  * (window > 0), and its page exists. A query that sees nothing gives zeros
  * (and lse = -infinity).
  * Scores, softmax and sums are FP32; queries enter the matrix product as FP16
- * after an exact scaling of each row by a power of two, probabilities as FP16
- * relative to the row's largest p_j * v_scale, codes exactly. One rounding
- * to the output type. Deterministic.
+ * after an exact scaling of each row by a power of two, codes exactly,
+ * probabilities as FP16 relative to the row's largest p_j * v_scale: off by at
+ * most 2^-11 of themselves down to 2^-23 of it, by 2^-34 of it below. One
+ * rounding to the output type. Deterministic.
  *   lens         int32 [batch] on the device; lengths above max_len or above
  *                table_width * page count as that
  *   max_tokens   at least the most queries of any sequence; max_len at least

@@ -76,6 +76,53 @@ def test_append_is_the_fp32_definition_bit_for_bit(lb, page, D, dt):
             assert s == scale and np.array_equal(have[:at], codes[:at])
 
 
+# ------------------------------------------------------------------ attention ---
+
+def _sinks(L, Hq, n, seed):
+    """Queries and a cache of which every 32nd token takes nearly all of the softmax
+    and has the value 0: what is left of the others, about 2^-24.6 each, is the result."""
+    P = Paged([L], 1, 16, 128, seed=seed)
+    g = np.random.default_rng(seed + 1)
+    q = g.standard_normal((n, Hq, 128))
+    q[:, :, 0] = 8
+    q = oracle.encode(q, "bf16")
+    codes = [od.block_codes(P.k[p, 0], "k", 16, 128) for p in range(P.pages)]
+    for p in range(P.pages):
+        codes[p][:, 0] = 0
+    for t in range(0, L, 32):                                  # the first token of every other page
+        p = P.table[0, t // 16]
+        codes[p][:] = 0
+        codes[p][0, 0] = 127
+        P.ks[p] = 17.3 / (128 ** -0.5 * 8 * 127)
+        v = od.block_codes(P.v[p, 0], "v", 16, 128)
+        v[0] = 0
+        P.v[p, 0] = od.block_bytes(v, "v").reshape(16, 128)
+    for p in range(P.pages):
+        P.k[p, 0] = od.block_bytes(codes[p], "k").reshape(16, 128)
+    return P, dev_bits(q, "bf16"), oracle.decode(q, "bf16")
+
+
+@pytest.mark.parametrize("n", [1, 30])
+def test_attention_keeps_what_sinks_leave(lb, n):
+    """Scores of 17.3 against normal ones: the other tokens' probabilities are
+    2^-24.6 e^s of a sink's, and all of the result. Relative 2-norm error: the BF16
+    output's rounding is at most 2^-9; FP16 probabilities above their normal range
+    add 2^-12 (independent roundings of at most 2^-11), and 2^-9.6 if no more than
+    seven powers of two lift a sink's above 1 (steps of 2^-31 of it). Together below 2^-8."""
+    banner(f"attention with sinks, {n} queries")
+    L, Hq = 4000, 4
+    P, q, hq = _sinks(L, Hq, n, 95)
+    out, lse = lb.attention(q, P.cache(lb), _i32(P.table), _i32([0, n]), _i32([L]), n, L, return_lse=True)
+    k, v = (od.cache_rows(*a, 0, L) for a in ((P.k, P.ks, P.table[0], "k"), (P.v, P.vs, P.table[0], "v")))
+    vs = P.vs[P.table[0][np.arange(L) // 16]].astype(np.float64)
+    want, we, _, _ = od.attention(hq, k, v, vs, L - n, 128 ** -0.5, True, 0)
+    O = to_host64(out)
+    off = np.linalg.norm(O - want, axis=2) / np.linalg.norm(want, axis=2)
+    print(f"relative error {off.max():.3g}")
+    assert (np.abs(to_host64(lse) - we) <= 2.0 ** -14 + 2.0 ** -22 * np.abs(we)).all()
+    assert off.max() <= 2.0 ** -8
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
