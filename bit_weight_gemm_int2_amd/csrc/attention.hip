@@ -8,9 +8,11 @@
 //  * Codes are integers of at most 127 and exact in FP16: byte u becomes
 //    0x6400 | u = 1024 + u by one byte permute for two codes, and a packed
 //    add takes 1152 off. Queries are scaled by a power of two per row (exact)
-//    so that BF16 ones keep their range, then rounded to FP16; every product
-//    is exact and sums are FP32.
-//  * Key scales multiply the FP32 scores. Value scales go into the softmax
+//    so that BF16 ones keep their range, then rounded to FP16 (exact down to
+//    2^-31 of the row's largest for BF16); every product is exact and sums are
+//    FP32.
+//  * The query's power of two and the softmax scale, then the key scales
+//    multiply the FP32 scores. Value scales go into the softmax
 //    exponent: with t_j = s_j + log2 s_v(j) (scores in powers of two) and the
 //    running maximum m of t_j, p'_j = 2^(t_j - m) needs no scaling per page in
 //    the values' product, and sum_j p_j is the FP32 sum of p'_j / s_v(j), taken
@@ -49,7 +51,7 @@ constexpr float NEG_INF = -__builtin_inff();
 
 struct Pages {
   int32_t blk[PAGES];                      // page * heads + head, 0 where there is no page
-  float kf[PAGES], lv[PAGES], rv[PAGES];   // key scale * scale, log2 and a unit's quotient of the value scale
+  float kf[PAGES], lv[PAGES], rv[PAGES];   // key scale, log2 and a unit's quotient of the value scale
 };
 
 // Two codes (bytes 0, 1 or 2, 3 of w) as FP16.
@@ -132,7 +134,7 @@ __device__ __forceinline__ void load_scales(const AttnArgs& a, int np, float uni
     const int32_t blk = pg->blk[i];
     const bool there = pg->lv[i] == 0.0f;
     const float ks = a.c.ks[blk], vs = fmaxf(a.c.vs[blk], MIN_SCALE);
-    pg->kf[i] = there ? ks * a.scale : 0.0f;
+    pg->kf[i] = there ? ks : 0.0f;
     pg->lv[i] = there ? __builtin_amdgcn_logf(vs) : NEG_INF;
     pg->rv[i] = unit / vs;
   }
@@ -148,12 +150,14 @@ __device__ __forceinline__ void values8(u32x4 w, float* x) {
   }
 }
 
-// The power of two that brings a row's largest magnitude into [1, 2), and its inverse.
-__device__ __forceinline__ void row_unit(float top, float* down, float* up) {
-  const int e = (int)(__builtin_bit_cast(uint32_t, top) >> 23);        // biased exponent; top >= 0
-  const bool use = e > 1 && e < 253;                                   // else (0, infinite) as it is
-  *down = use ? __builtin_bit_cast(float, (uint32_t)(254 - e) << 23) : 1.0f;
-  *up = use ? __builtin_bit_cast(float, (uint32_t)e << 23) : 1.0f;
+// The power of two that brings a row's largest magnitude into [2^14, 2^15), the
+// top of FP16's range, and its inverse. Both stay normal numbers: a row below
+// 2^-112 comes to lie lower (at 2^-7 with the smallest BF16 value), one with
+// an infinity keeps it.
+__device__ __forceinline__ void row_unit(float top, float* by, float* back) {
+  const int e = min(max((int)(__builtin_bit_cast(uint32_t, top) >> 23), 15), 254);   // biased exponent; top >= 0
+  *by = __builtin_bit_cast(float, (uint32_t)(268 - e) << 23);
+  *back = __builtin_bit_cast(float, (uint32_t)(e - 14) << 23);
 }
 
 template <bool BF16>
@@ -251,14 +255,15 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 #pragma unroll
           for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[i][k][e]));
         }
-      float down;
-      row_unit(max16(top), &down, &qs);
+      float by;
+      row_unit(max16(top), &by, &qs);
+      qs *= a.scale;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) qf[i][k][e] = pack2(x[i][k][2 * e] * down, x[i][k][2 * e + 1] * down);
+          for (int e = 0; e < 4; ++e) qf[i][k][e] = pack2(x[i][k][2 * e] * by, x[i][k][2 * e + 1] * by);
     }
     const int pos = w.pos(w.row0 + min(r, w.rows - 1), a.group);
     const int hi = a.causal ? min(w.t1, pos + 1) : w.t1, lo = a.window ? pos - a.window + 1 : 0;
@@ -451,19 +456,20 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
     for (int s = 0; s < D / 16; ++s) qf[s] = *(const u32x4*)((const uint16_t*)a.q.p + at + 16 * s);
   }
   auto convert_queries = [&]() __attribute__((always_inline)) {
-    float x[8], top = 0.0f, down;
+    float x[8], top = 0.0f, by;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       values8<BF16>(qf[s], x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
     }
-    row_unit(max32(top), &down, &qs);
+    row_unit(max32(top), &by, &qs);
+    qs *= a.scale;
 #pragma unroll
     for (int s = 0; s < D / 16; ++s) {
       values8<BF16>(qf[s], x);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) qf[s][e] = pack2(x[2 * e] * down, x[2 * e + 1] * down);
+      for (int e = 0; e < 4; ++e) qf[s][e] = pack2(x[2 * e] * by, x[2 * e + 1] * by);
     }
   };
   const int pos = w.pos(w.row0 + rr, a.group);

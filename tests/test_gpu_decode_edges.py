@@ -123,6 +123,31 @@ def test_attention_keeps_what_sinks_leave(lb, n):
     assert off.max() <= 2.0 ** -8
 
 
+@pytest.mark.parametrize("n", [1, 50])
+@pytest.mark.parametrize("power", [125, 126, 127, -120, -126])
+def test_attention_bf16_queries_at_the_ends_of_the_range(lb, n, power):
+    """Rows whose largest magnitude is 2^power .. 2^(power + 1), with key scales and
+    the softmax scale that bring the scores back to order 1 (each a normal number)."""
+    banner(f"attention, bf16 queries of 2^{power}, {n} queries")
+    P = Paged([150], 2, 32, 64, seed=100)
+    half = 20 if power > 0 else -20
+    P.ks[:] = P.ks * np.float32(2.0 ** -half)
+    g = np.random.default_rng(101)
+    q = g.uniform(-1, 1, (n, 4, 64))
+    q[:, :, 7] = 1.5                                           # the row's largest: 1.5 2^power
+    q = oracle.encode(q * 2.0 ** power, "bf16")
+    hq, scale = oracle.decode(q, "bf16"), 0.125 * 2.0 ** (half - power)
+    out, lse = lb.attention(dev_bits(q, "bf16"), P.cache(lb), _i32(P.table), _i32([0, n]), _i32([150]), n, 150,
+                            scale=scale, return_lse=True)
+    k, v = (od.cache_rows(*a, 0, 150) for a in ((P.k, P.ks, P.table[0], "k"), (P.v, P.vs, P.table[0], "v")))
+    vs = P.vs[P.table[0][np.arange(150) // 32]].astype(np.float64)
+    want, we, mag, peak = od.attention(hq, k, v, vs, 150 - n, scale, True, 0)
+    O = to_host64(out)
+    bound = 2.0 ** -10 * mag + 2.0 ** -25 * peak + _half_ulp(np.maximum(np.abs(want), np.abs(O)), out.dtype)
+    assert (np.abs(O - want) <= bound).all()
+    assert (np.abs(to_host64(lse) - we) <= 2.0 ** -14 + 2.0 ** -22 * np.abs(we)).all()
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
