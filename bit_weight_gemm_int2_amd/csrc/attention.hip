@@ -46,7 +46,11 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
 constexpr int PAGES = 264;                 // pages of one segment whose scales are held in LDS
 constexpr float LN2 = 0.69314718055994530942f;
-constexpr float MIN_SCALE = 7.888609052210118e-31f;   // 2^-100: scales below are all-zero blocks
+// Value scales below 2^-100 are those of all-zero blocks, whose tokens have
+// weight and no value. They count as 2^-64: with the other scales between 2^-64
+// and 2^40, neither p' / s_v of an equal score leaves FP32's range nor do the
+// zeros push the others' p' below FP16's.
+constexpr float MIN_SCALE = 0x1p-100f, ZERO_SCALE = 0x1p-64f;
 constexpr float NEG_INF = -__builtin_inff();
 
 struct Pages {
@@ -133,7 +137,7 @@ __device__ __forceinline__ void load_scales(const AttnArgs& a, int np, float uni
   for (int i = threadIdx.x; i < np; i += blockDim.x) {
     const int32_t blk = pg->blk[i];
     const bool there = pg->lv[i] == 0.0f;
-    const float ks = a.c.ks[blk], vs = fmaxf(a.c.vs[blk], MIN_SCALE);
+    const float ks = a.c.ks[blk], vs = a.c.vs[blk] >= MIN_SCALE ? a.c.vs[blk] : ZERO_SCALE;
     pg->kf[i] = there ? ks : 0.0f;
     pg->lv[i] = there ? __builtin_amdgcn_logf(vs) : NEG_INF;
     pg->rv[i] = unit / vs;

@@ -444,7 +444,9 @@ int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table,
  * after an exact scaling of each row by a power of two, codes exactly,
  * probabilities as FP16 relative to the row's largest p_j * v_scale: off by at
  * most 2^-11 of themselves down to 2^-23 of it, by 2^-34 of it below. One
- * rounding to the output type. Deterministic.
+ * rounding to the output type. Deterministic. The value scales that a query
+ * sees may lie up to 2^100 apart, those beside blocks of scale 0 (all-zero,
+ * with full weight in the sum) between 2^-64 and 2^40.
  *   lens         int32 [batch] on the device; lengths above max_len or above
  *                table_width * page count as that
  *   max_tokens   at least the most queries of any sequence; max_len at least

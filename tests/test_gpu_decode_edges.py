@@ -148,6 +148,48 @@ def test_attention_bf16_queries_at_the_ends_of_the_range(lb, n, power):
     assert (np.abs(to_host64(lse) - we) <= 2.0 ** -14 + 2.0 ** -22 * np.abs(we)).all()
 
 
+@pytest.mark.parametrize("n", [1, 100])
+@pytest.mark.parametrize("power", [-64, -30, 0, 30, 40])
+def test_attention_all_zero_blocks_keep_their_weight(lb, n, power):
+    """Equal scores over one block of values and one whose scale is 0: the mean of
+    all 32 tokens, whatever the other block's scale. Probabilities are equal powers
+    of two or their neighbours: 2^-10 sum p |v| / sum p and half an output ulp."""
+    banner(f"attention, zero block beside scale 2^{power}, {n} queries")
+    P = Paged([32], 1, 16, 64, seed=96)
+    P.k[:] = 128
+    a, b = P.table[0]
+    P.vs[a], P.vs[b] = 2.0 ** power, 0
+    P.v[b] = 128
+    q, _ = _values(np.random.default_rng(97), (n, 1, 64), "bf16")
+    out, lse = lb.attention(q, P.cache(lb), _i32(P.table), _i32([0, n]), _i32([32]), n, 32, causal=False,
+                            return_lse=True)
+    v = od.block_codes(P.v[a, 0], "v", 16, 64) * 2.0 ** power
+    want = np.broadcast_to(v.sum(0) / 32, (n, 1, 64))
+    O = to_host64(out)
+    bound = 2.0 ** -10 * np.abs(v).sum(0) / 32 + _half_ulp(np.maximum(np.abs(want), np.abs(O)), out.dtype)
+    assert (np.abs(O - want) <= bound).all()
+    assert (np.abs(to_host64(lse) - np.log(32)) <= 2.0 ** -14).all()
+
+
+@pytest.mark.parametrize("n", [1, 100])
+def test_attention_value_scales_a_hundred_powers_apart(lb, n):
+    """Equal scores over blocks of scale 2^-60 and 2^40: each token has 1/32 of the sum."""
+    banner(f"attention, value scales 2^100 apart, {n} queries")
+    P = Paged([32], 1, 16, 64, seed=98)
+    P.k[:] = 128
+    a, b = P.table[0]
+    P.vs[a], P.vs[b] = 2.0 ** 40, 2.0 ** -60
+    q, _ = _values(np.random.default_rng(99), (n, 1, 64), "bf16")
+    out, lse = lb.attention(q, P.cache(lb), _i32(P.table), _i32([0, n]), _i32([32]), n, 32, causal=False,
+                            return_lse=True)
+    v = od.block_codes(P.v[a, 0], "v", 16, 64) * 2.0 ** 40
+    O = to_host64(out)
+    want = np.broadcast_to(v.sum(0) / 32, (n, 1, 64))
+    bound = 2.0 ** -10 * (np.abs(v).sum(0) + 1) / 32 + _half_ulp(np.maximum(np.abs(want), np.abs(O)), out.dtype)
+    assert (np.abs(O - want) <= bound).all()
+    assert (np.abs(to_host64(lse) - np.log(32)) <= 2.0 ** -14).all()
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
