@@ -595,7 +595,8 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
     cu_tokens[b+1] - 1 and go to positions starts[b], ...; max_tokens is a
     host bound on the rows of one sequence. cos, sin: float32 [positions,
     rot/2], both or none. bad_count: int32 [2], added to: non-finite values
-    (stored as 0) and tokens left out (no page or no position)."""
+    (stored as 0) and tokens left out (no page or no position; a query
+    without a position comes back as zeros)."""
     if k.dim() != 3:
         raise ValueError("k must be [tokens, kv_heads, head_dim]")
     shape, dtype = k.shape, k.dtype

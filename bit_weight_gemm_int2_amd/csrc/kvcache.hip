@@ -333,12 +333,23 @@ __device__ void append_values(const KvAppendArgs& g, int64_t row0, int p0, int n
   if (threadIdx.x == 0) *sp = s.s;
 }
 
-// Rotate the queries of n tokens (heads first .. last - 1). A thread takes one
+// Rotate the queries of n tokens (heads first .. last - 1), the first
+// `rotated` of which have a position; the others' become 0. A thread takes one
 // unit of one token and walks the heads with its cos and sin in registers;
 // with few tokens the heads are spread over threads too.
 template <int DT>
-__device__ void rotate_queries(const KvAppendArgs& g, int64_t row0, int64_t pos0, int n, int first, int last) {
-  const int U = g.c.D / 16, shift = 31 - __builtin_clz(U), units = n << shift;
+__device__ void rotate_queries(const KvAppendArgs& g, int64_t row0, int64_t pos0, int n, int rotated, int first,
+                               int last) {
+  const int U = g.c.D / 16, shift = 31 - __builtin_clz(U), units = rotated << shift;
+  const float zeros[8] = {};
+  for (int i = threadIdx.x + units; i < n << shift; i += blockDim.x) {
+    const int64_t to = (row0 + (i >> shift)) * g.qo.ts + 16 * (i & (U - 1));
+    for (int h = first; h < last; ++h) {
+      store8<DT>(g.qo.p, to + h * g.qo.hs, zeros);
+      store8<DT>(g.qo.p, to + h * g.qo.hs + 8, zeros);
+    }
+  }
+  if (!units) return;
   const int ways = max(1, min(last - first, (int)blockDim.x / units));
   for (int i = threadIdx.x; i < units * ways; i += blockDim.x) {
     const int way = i / units, j = i - way * units, t = j >> shift, u = j & (U - 1);
@@ -379,7 +390,7 @@ __global__ __launch_bounds__(MAX_THREADS) void append_kernel(KvAppendArgs g, int
   const int rotated = (int)max((int64_t)0, known - first);   // of the n tokens
   if (role >= 2 * H) {
     const int h0 = (role - 2 * H) * q_group;
-    rotate_queries<DT>(g, row0, first, rotated, h0, min(g.q_heads, h0 + q_group));
+    rotate_queries<DT>(g, row0, first, n, rotated, h0, min(g.q_heads, h0 + q_group));
     return;
   }
   const int64_t id = slot < g.t.width ? g.t.table[b * g.t.width + slot] : -1;

@@ -387,8 +387,8 @@ typedef struct {
  * its new scale. The result is a pure function of the input. NaN and infinite
  * values (after the rotation) are stored as 0 and counted in bad_count[0];
  * tokens whose page entry is no page, or whose position is not in the tables,
- * are left out and counted in bad_count[1] (once each; a query without a
- * position is not written). Two sequences may share a page only when neither
+ * are left out and counted in bad_count[1] (once each); the query of a token
+ * without a position becomes zeros. Two sequences may share a page only when neither
  * appends to it in this call.
  *   block_table  int32 [batch][table_width]; cu_tokens int32 [batch + 1],
  *                rising from 0 to `tokens`; starts int32 [batch], >= 0 (all

@@ -9,7 +9,7 @@ import oracle
 import workloads as wl
 from oracle import paged as od
 from gpu_util import TORCH_DT, banner, dev_bits, to_host64
-from test_gpu_decode import Paged, _attend, _f16, _gemv_check, _half_ulp, _i32, _values, lb  # noqa: F401
+from test_gpu_decode import Paged, _attend, _f16, _gemv_check, _half_ulp, _i32, _rope, _values, lb  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -74,6 +74,32 @@ def test_append_is_the_fp32_definition_bit_for_bit(lb, page, D, dt):
         at, scale = at + n, new
         for have, s in _codes_and_scale(cache, page, D):
             assert s == scale and np.array_equal(have[:at], codes[:at])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_append_queries_without_a_position_become_zeros(lb, dt, in_place):
+    """Tables of 20 positions: tokens 20 .. 39 have none, the last page no token with one."""
+    banner(f"append, queries past the tables, {dt}, in place {in_place}")
+    H, Hq, page, D = 2, 5, 16, 64
+    g = np.random.default_rng(90)
+    x, _ = _values(g, (40, Hq + 2 * H, D), dt)
+    cos, sin = (torch.from_numpy(a).cuda() for a in _rope(40, D))
+    res = []
+    for rows in (40, 20):
+        y, cache = x.clone(), lb.new_kv_cache(3, H, page, D)
+        q = y[:, :Hq] if in_place else x[:, :Hq]
+        out = q if in_place else torch.full((40, Hq, D), 7.0, dtype=x.dtype, device="cuda")
+        bad = torch.zeros(2, dtype=torch.int32, device="cuda")
+        lb.kv_append(x[:, Hq:Hq + H], x[:, Hq + H:], cache, _i32([[2, 0, 1]]), _i32([0, 40]), _i32([0]), 40, q=q,
+                     cos=cos[:rows].contiguous(), sin=sin[:rows].contiguous(), q_out=out, bad_count=bad)
+        assert bad.tolist() == [0, 40 - rows]
+        assert torch.equal(y[:, Hq:], x[:, Hq:])
+        res.append((out.clone(), cache))
+    (full, c0), (cut, c1) = res
+    assert torch.equal(cut[:20], full[:20]) and (cut[20:] == 0).all() and (full[20:] != 0).any()
+    assert torch.equal(c0.k[2], c1.k[2]) and torch.equal(c0.v[2], c1.v[2])
+    assert (c1.k[1] == 0).all() and (c1.v[1] == 0).all()                   # the last page stays as it was
 
 
 # ------------------------------------------------------------------ attention ---
