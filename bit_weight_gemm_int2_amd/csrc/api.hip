@@ -623,7 +623,9 @@ bool any_overlap(Range a, std::initializer_list<Range> others) {
 // Checks shared by the calls on the paged cache.
 int32_t check_cache(const lowbit_kv_cache* c, const int32_t* table, int64_t width, const int32_t* cu,
                     const int32_t* start, int64_t batch, int64_t tokens, int64_t max_tokens) {
-  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale || !cu || !start || (!table && width)) return LOWBIT_ERR_NULL;
+  if (!c || !c->k || !c->v || !c->k_scale || !c->v_scale) return LOWBIT_ERR_NULL;
+  // an empty batch has empty arrays, which may have no address
+  if ((batch || tokens) && (!cu || !start || (!table && width))) return LOWBIT_ERR_NULL;
   if (c->pages < 1 || c->kv_heads < 1 || c->kv_heads > 4096 || c->pages >= kMaxDim ||
       c->pages * c->kv_heads >= kMaxDim)
     return LOWBIT_ERR_SHAPE;

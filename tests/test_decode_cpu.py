@@ -202,6 +202,24 @@ def test_attention_workspace_query(b):
     assert f(64, 64 * 512, 512, 4096, 32, 8, 128, 0) == 0     # prompts that fill the GPU are not split
 
 
+@made_up_addresses
+def test_an_empty_batch_needs_no_addresses(b):
+    """No sequences and no tokens: the arrays are empty, and an empty array's address may be null."""
+    L, none = b.lib(), (None, 7, None, None, 0, 0, 0)
+    assert L.lowbit_kv_append(_cache(b), *none, b.BF16, None, 512, 128, None, 512, 128, None, 0, 0, 0, None, 0, 0, None,
+                              None, 0, 0, 0, None, None) == b.OK
+    assert L.lowbit_kv_read(_cache(b), *none, b.F32, None, 512, 128, None, 512, 128, None) == b.OK
+    assert L.lowbit_attention(_cache(b), *none, 0, b.F16, None, 1024, 128, 8, None, 1024, 128, None, 0.1, 1, 0, None, 0,
+                              None) == b.OK
+    some = (None, 7, None, None, 0, 3, 3)                     # tokens of no sequence
+    assert L.lowbit_kv_read(_cache(b), *some, b.F32, P, 512, 128, P, 512, 128, None) == b.ERR_NULL
+    for i in range(3):                                        # sequences without their arrays
+        ptr = [P + (4 << 32), P + (5 << 32), P + (6 << 32)]
+        ptr[i] = None
+        assert L.lowbit_kv_read(_cache(b), ptr[0], 7, ptr[1], ptr[2], 2, 0, 0, b.F32, None, 512, 128, None, 512, 128,
+                                None) == b.ERR_NULL
+
+
 def test_python_refusals(b):
     cpu = torch.zeros((2, 1, 16, 64), dtype=torch.uint8)
     s = torch.zeros((2, 1))

@@ -102,6 +102,21 @@ def test_append_queries_without_a_position_become_zeros(lb, dt, in_place):
     assert (c1.k[1] == 0).all() and (c1.v[1] == 0).all()                   # the last page stays as it was
 
 
+@pytest.mark.parametrize("width", [0, 5])
+def test_an_empty_batch_gives_empty_results(lb, width):
+    """A scheduler's step without sequences: every array is empty."""
+    banner(f"empty batch, table width {width}")
+    cache = lb.new_kv_cache(3, 2, 16, 64)
+    x = torch.empty((0, 8, 64), dtype=torch.bfloat16, device="cuda")
+    e = [torch.empty(shape, dtype=torch.int32, device="cuda") for shape in ((0, width), (0,))]
+    cu = _i32([0])
+    cos, sin = (torch.from_numpy(a).cuda() for a in _rope(20, 64))
+    q = lb.kv_append(x[:, 4:6], x[:, 6:], cache, e[0], cu, e[1], 0, q=x[:, :4], cos=cos, sin=sin)
+    k, v = lb.kv_read(cache, e[0], cu, e[1], 0, 0)
+    y, lse = lb.attention(x[:, :4], cache, e[0], cu, e[1], 0, 0, return_lse=True)
+    assert q.shape == y.shape == (0, 4, 64) and k.shape == v.shape == (0, 2, 64) and lse.shape == (0, 4)
+
+
 # ------------------------------------------------------------------ attention ---
 
 def _sinks(L, Hq, n, seed):
