@@ -148,6 +148,19 @@ def new_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
     return ws
 
 
+def _given_workspace(workspace: torch.Tensor, need: int, what: str) -> int:
+    """The bytes of a workspace given by the caller: one dense block of GPU
+    memory (the elements of an expanded or strided tensor count more bytes
+    than it owns, or others than those behind its address)."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    _cuda(workspace, "workspace")
+    size = workspace.numel() * workspace.element_size()
+    if size < need:
+        raise ValueError(f"workspace holds {size} bytes, {what} needs {need}")
+    return size
+
+
 def _shared_workspace(device: torch.device, nbytes: int, stream) -> torch.Tensor:
     """A workspace per (device, stream), reused by every call on that stream
     that passes none: calls on one stream never overlap, and calls on two
@@ -241,13 +254,11 @@ def gemm_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
     need = int(lib().lowbit_gemm_int4_workspace_bytes(M, N, K))
     if workspace is None:
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device=x.device)
-    elif workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, "
-                         f"lowbit_gemm_int4 needs {need}")
+    size = _given_workspace(workspace, need, "lowbit_gemm_int4")
     _check(lib().lowbit_gemm_int4(
         x.data_ptr(), _DT[x.dtype], M, K, x.stride(0), packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
         GROUP, N, _ptr(bias), NONE if bias is None else _DT[bias.dtype], out.data_ptr(), _DT[out.dtype],
-        out.stride(0), _ACT[activation], workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        out.stride(0), _ACT[activation], workspace.data_ptr(), size,
         _stream(stream)), "lowbit_gemm_int4")
     return out
 
@@ -361,16 +372,13 @@ def gemm(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, fmt, bias:
     ws_need = workspace_bytes(fmt, M, N, K)
     if ws_need and workspace is None:
         workspace = _shared_workspace(x.device, ws_need, stream)
-    elif ws_need and workspace.numel() * workspace.element_size() < ws_need:
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, "
-                         f"lowbit_gemm needs {ws_need}")
+    size = 0 if workspace is None else _given_workspace(workspace, ws_need, "lowbit_gemm")
     st = lib().lowbit_gemm(
         _FMT[fmt], x.data_ptr(), _DT[x.dtype], M, K, x.stride(0),
         packed.data_ptr(), scales.data_ptr(), GROUP, N,
         _ptr(bias), NONE if bias is None else _DT[bias.dtype],
         out.data_ptr(), _DT[out.dtype], out.stride(0), _ACT[activation],
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream(stream))
+        _ptr(workspace), size, _stream(stream))
     _check(st, "lowbit_gemm")
     return out
 
@@ -420,16 +428,13 @@ def gemm_grouped(xs, packeds, scales, fmt, biases=None, out_dtype: Optional[torc
     need = int(lib().lowbit_gemm_grouped_workspace_bytes(count, _FMT[fmt], M, N, K))
     if need and workspace is None:
         workspace = _shared_workspace(x0.device, need, stream)
-    elif need and workspace.numel() * workspace.element_size() < need:
-        raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, "
-                         f"lowbit_gemm_grouped needs {need}")
+    size = 0 if workspace is None else _given_workspace(workspace, need, "lowbit_gemm_grouped")
     st = lib().lowbit_gemm_grouped(
         count, _FMT[fmt], _ptr_array([x.data_ptr() for x in xs]), _DT[x0.dtype], M, K, x0.stride(0),
         _ptr_array([p.data_ptr() for p in packeds]), _ptr_array([s_.data_ptr() for s_ in scales]), GROUP, N,
         None if biases is None else _ptr_array([b.data_ptr() for b in biases]), bdt,
         _ptr_array([y.data_ptr() for y in outs]), _DT[outs[0].dtype], outs[0].stride(0), _ACT[activation],
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
-        _stream(stream))
+        _ptr(workspace), size, _stream(stream))
     _check(st, "lowbit_gemm_grouped")
     return outs
 
@@ -696,10 +701,7 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
     need = L.lowbit_attention_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window)
     size = 0
     if workspace is not None:
-        _cuda(workspace, "workspace")
-        size = workspace.numel() * workspace.element_size()
-        if size < need:
-            raise ValueError(f"workspace holds {size} bytes, lowbit_attention needs {need}")
+        size = _given_workspace(workspace, need, "lowbit_attention")
     elif need:
         workspace, size = _new(need, torch.uint8, q, stream), need
     _check(L.lowbit_attention(cache.ref, *head, T, max_tokens, max_len, _DT[dtype], *qa, Hq, *oa, _ptr(lse),

@@ -231,3 +231,12 @@ def test_python_refusals(b):
         b.KVCache(cpu, cpu, s[:1], s)
     with pytest.raises(ValueError):
         b.gemv_int4(torch.zeros(1, 128), torch.zeros((4, 64), dtype=torch.uint8), s, s)
+
+
+def test_a_workspace_is_one_dense_block(b):
+    """One byte expanded to 4096, and every other byte of a block, are not 4096 bytes to write to."""
+    for t in (torch.empty(1, dtype=torch.uint8).expand(4096), torch.empty(8192, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="contiguous"):
+            b._given_workspace(t, 4096, "a call")
+    with pytest.raises(ValueError, match="GPU"):
+        b._given_workspace(torch.empty(4096, dtype=torch.uint8), 4096, "a call")

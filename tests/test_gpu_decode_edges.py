@@ -231,6 +231,22 @@ def test_attention_value_scales_a_hundred_powers_apart(lb, n):
     assert (np.abs(to_host64(lse) - np.log(32)) <= 2.0 ** -14).all()
 
 
+def test_attention_workspaces(lb):
+    """A given workspace of just the bytes needed works; a strided or expanded one that
+    counts as many elements, and a smaller one, are refused."""
+    banner("attention workspaces")
+    P, n, L = Paged([3000], 1, 16, 64, seed=102), 2, 3000
+    q, _ = _values(np.random.default_rng(103), (n, 2, 64), "f16")
+    need = lb.lib().lowbit_attention_workspace_bytes(1, n, n, L, 2, 1, 64, 0)
+    assert need
+    call = lambda ws: lb.attention(q, P.cache(lb), _i32(P.table), _i32([0, n]), _i32([L]), n, L, workspace=ws)  # noqa: E731
+    assert torch.equal(call(torch.empty(need, dtype=torch.uint8, device="cuda")), call(None))
+    one = torch.empty(1, dtype=torch.uint8, device="cuda")
+    for ws in (one.expand(need), torch.empty(2 * need, dtype=torch.uint8, device="cuda")[::2], one):
+        with pytest.raises(ValueError, match="workspace"):
+            call(ws)
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
