@@ -458,7 +458,18 @@ def _queue(stream, device: int) -> int:
     """The HIP stream of a call: `stream`, or the current stream of the
     operands' device (taken as a number: a decoding step makes many short
     calls, and the stream object of torch.cuda.current_stream costs 2 us)."""
-    return torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device)
+    if stream.device_index != device:
+        raise ValueError(f"the stream is of GPU {stream.device_index}, the operands are on GPU {device}")
+    return stream.cuda_stream
+
+
+def _same_device(device: int, **operands):
+    """The error of operands that are not all GPU tensors of one device."""
+    on = ", ".join(f"{n} on {t.device}" for n, t in operands.items() if t.get_device() != device)
+    where = f"GPU {device} like the first operand" if device >= 0 else "a GPU"
+    return ValueError(f"every operand must be on {where}" + (f"; {on}" if on else ""))
 
 
 def _new(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
@@ -488,8 +499,12 @@ def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
     reads the codes once, no workspace.
 
     x: [M, K] fp16/bf16; packed: [N, K/2] uint8; scales, zeros: fp16 [N, K/128]."""
-    if not (x.is_cuda and packed.is_cuda and scales.is_cuda and zeros.is_cuda):
-        raise ValueError("x, packed, scales and zeros must be GPU tensors")
+    dev = x.get_device()
+    if not 0 <= dev == packed.get_device() == scales.get_device() == zeros.get_device():
+        raise _same_device(dev, packed=packed, scales=scales, zeros=zeros)
+    if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
+        with torch.cuda.device(dev):
+            return gemv_int4(x, packed, scales, zeros, bias, out_dtype, activation, out, stream)
     xdt = _DT.get(x.dtype)
     if x.dim() != 2 or (xdt != F16 and xdt != BF16):
         raise ValueError("x must be 2-D float16 or bfloat16 with unit stride along K")
@@ -506,7 +521,8 @@ def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
             raise ValueError(f"{nm} must be float16 [{N}, {K // GROUP}]")
     bdt = NONE
     if bias is not None:
-        _cuda(bias, "bias")
+        if bias.get_device() != dev:
+            raise _same_device(dev, bias=bias)
         bias = _dense(bias, stream)
         if bias.numel() != N or bias.dtype not in _DT:
             raise ValueError(f"bias must hold {N} float16, bfloat16 or float32 values")
@@ -514,14 +530,15 @@ def gemv_int4(x: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, zeros
     if out is None:
         out, ldy = _new((M, N), x.dtype if out_dtype is None else out_dtype, x, stream), N
     else:
-        _cuda(out, "out")
+        if out.get_device() != dev:
+            raise _same_device(dev, out=out)
         if out.shape != (M, N) or out.stride(1) != 1 or out.dtype not in _DT:
             raise ValueError(f"out must be [{M}, {N}] with unit stride along N")
         ldy = out.stride(0)
     _check(lib().lowbit_gemv_int4(
         x.data_ptr(), xdt, M, K, ldx if M > 1 else K, packed.data_ptr(), scales.data_ptr(), zeros.data_ptr(),
         GROUP, N, _ptr(bias), bdt, out.data_ptr(), _DT[out.dtype], ldy, _ACT[activation],
-        _queue(stream, x.get_device())), "lowbit_gemv_int4")
+        _queue(stream, dev)), "lowbit_gemv_int4")
     return out
 
 
@@ -537,7 +554,7 @@ class KVCache:
     layout of include/lowbit.h; k_scale, v_scale: float32 [pages, kv_heads].
     Made by new_kv_cache, filled by kv_append, read by attention and kv_read."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "kv_heads", "page", "head_dim", "struct", "ref")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "kv_heads", "page", "head_dim", "device", "struct", "ref")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         shape = k.shape
@@ -549,9 +566,12 @@ class KVCache:
         if (k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != shape
                 or v_scale.shape != shape):
             raise ValueError(f"k_scale and v_scale must be float32 [{pages}, {heads}]")
+        self.device = dev = k.get_device()
+        if not 0 <= dev == v.get_device() == k_scale.get_device() == v_scale.get_device():
+            raise _same_device(dev, v=v, k_scale=k_scale, v_scale=v_scale)
         for t in (k, v, k_scale, v_scale):
-            if not (t.is_cuda and t.is_contiguous()):
-                raise ValueError("k, v, k_scale and v_scale must be contiguous GPU tensors")
+            if not t.is_contiguous():
+                raise ValueError("k, v, k_scale and v_scale must be contiguous")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
         self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                    pages, heads, page, d)
@@ -566,10 +586,10 @@ def new_kv_cache(pages: int, kv_heads: int, page: int, head_dim: int, device=Non
     return KVCache(k, v, ks, vs)
 
 
-def _table(block_table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, what: str):
-    """Arguments that every call on the cache begins with, checked."""
-    if not (block_table.is_cuda and cu.is_cuda and start.is_cuda):
-        raise ValueError(f"block_table, cu_tokens and {what} must be GPU tensors")
+def _table(dev: int, block_table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, what: str):
+    """Arguments that every call on the cache begins with, checked; `dev` is the cache's GPU."""
+    if not dev == block_table.get_device() == cu.get_device() == start.get_device():
+        raise _same_device(dev, block_table=block_table, cu_tokens=cu, **{what: start})
     if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_contiguous():
         raise ValueError("block_table must be a contiguous int32 tensor [batch, pages of a sequence]")
     batch, width = block_table.shape
@@ -580,10 +600,12 @@ def _table(block_table: torch.Tensor, cu: torch.Tensor, start: torch.Tensor, wha
     return block_table.data_ptr(), width, cu.data_ptr(), start.data_ptr(), batch
 
 
-def _rows3(t: torch.Tensor, shape, dtype, name: str):
+def _rows3(dev: int, t: torch.Tensor, shape, dtype, name: str):
     ts, hs, unit = t.stride() if t.dim() == 3 else (0, 0, 0)
-    if not t.is_cuda or t.shape != shape or t.dtype != dtype or (unit != 1 and shape[0]):
-        raise ValueError(f"{name} must be a GPU tensor {dtype} {list(shape)} with unit stride along the last dimension")
+    if t.get_device() != dev:
+        raise _same_device(dev, **{name: t})
+    if t.shape != shape or t.dtype != dtype or (unit != 1 and shape[0]):
+        raise ValueError(f"{name} must be {dtype} {list(shape)} with unit stride along the last dimension")
     return t.data_ptr(), ts, hs
 
 
@@ -610,16 +632,21 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
         raise ValueError(f"the cache holds {cache.kv_heads} heads of {cache.head_dim}, k has {H} of {D}")
     if dtype not in _DT:
         raise ValueError("k must be float16, bfloat16 or float32")
-    head = _table(block_table, cu_tokens, starts, "starts")
-    ka, va = _rows3(k, shape, dtype, "k"), _rows3(v, shape, dtype, "v")
+    dev = cache.device
+    if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
+        with torch.cuda.device(dev):
+            return kv_append(k, v, cache, block_table, cu_tokens, starts, max_tokens, q, cos, sin, interleaved, q_out,
+                             bad_count, stream)
+    head = _table(dev, block_table, cu_tokens, starts, "starts")
+    ka, va = _rows3(dev, k, shape, dtype, "k"), _rows3(dev, v, shape, dtype, "v")
     if q is not None:
         Hq = q.shape[1]
-        qa = _rows3(q, (T, Hq, D), dtype, "q")
+        qa = _rows3(dev, q, (T, Hq, D), dtype, "q")
         if q_out is None:
             q_out = _new((T, Hq, D), dtype, k, stream)
             qo = q_out.data_ptr(), Hq * D, D
         else:
-            qo = _rows3(q_out, (T, Hq, D), dtype, "q_out")
+            qo = _rows3(dev, q_out, (T, Hq, D), dtype, "q_out")
     else:
         if q_out is not None:
             raise ValueError("q_out without q")
@@ -631,17 +658,20 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
         if cos.dim() != 2 or sin.shape != cos.shape:
             raise ValueError("cos and sin must be [positions, rot/2]")
         for t in (cos, sin):
-            if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous():
-                raise ValueError("cos and sin must be contiguous float32 GPU tensors")
+            if t.get_device() != dev:
+                raise _same_device(dev, cos=cos, sin=sin)
+            if t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError("cos and sin must be contiguous float32 tensors")
         positions, rot = cos.shape
         rot *= 2
     if bad_count is not None:
-        _cuda(bad_count, "bad_count")
+        if bad_count.get_device() != dev:
+            raise _same_device(dev, bad_count=bad_count)
         if bad_count.dtype != torch.int32 or bad_count.numel() != 2 or not bad_count.is_contiguous():
             raise ValueError("bad_count must be int32 [2]")
     _check(lib().lowbit_kv_append(cache.ref, *head, T, max_tokens, _DT[dtype], *ka, *va, *qa, Hq, *qo, _ptr(cos),
                                   _ptr(sin), rot, positions, interleaved, _ptr(bad_count),
-                                  _queue(stream, k.get_device())), "lowbit_kv_append")
+                                  _queue(stream, dev)), "lowbit_kv_append")
     return q_out
 
 
@@ -656,15 +686,19 @@ def kv_read(cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor, 
         raise ValueError("dtype must be float16, bfloat16 or float32")
     H, D = cache.kv_heads, cache.head_dim
     shape = (tokens, H, D)
-    head = _table(block_table, cu_tokens, starts, "starts")
+    dev = cache.device
+    if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
+        with torch.cuda.device(dev):
+            return kv_read(cache, block_table, cu_tokens, starts, tokens, max_tokens, dtype, out, stream)
+    head = _table(dev, block_table, cu_tokens, starts, "starts")
     if out is None:
         k, v = _new(shape, dtype, cache.k, stream), _new(shape, dtype, cache.k, stream)
         ka, va = (k.data_ptr(), H * D, D), (v.data_ptr(), H * D, D)
     else:
         k, v = out
-        ka, va = _rows3(k, shape, dtype, "k"), _rows3(v, shape, dtype, "v")
+        ka, va = _rows3(dev, k, shape, dtype, "k"), _rows3(dev, v, shape, dtype, "v")
     _check(lib().lowbit_kv_read(cache.ref, *head, tokens, max_tokens, _DT[dtype], *ka, *va,
-                                _queue(stream, cache.k.get_device())), "lowbit_kv_read")
+                                _queue(stream, dev)), "lowbit_kv_read")
     return k, v
 
 
@@ -689,22 +723,29 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
     H = cache.kv_heads
     if cache.head_dim != D or Hq % H:
         raise ValueError(f"the cache holds {H} heads of {cache.head_dim}, q has {Hq} of {D}")
-    head = _table(block_table, cu_tokens, lens, "lens")
-    qa = _rows3(q, shape, dtype, "q")
+    dev = cache.device
+    if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
+        with torch.cuda.device(dev):
+            return attention(q, cache, block_table, cu_tokens, lens, max_tokens, max_len, scale, causal, window, out,
+                             return_lse, workspace, stream)
+    head = _table(dev, block_table, cu_tokens, lens, "lens")
+    qa = _rows3(dev, q, shape, dtype, "q")
     if out is None:
         out = _new(shape, dtype, q, stream)
         oa = out.data_ptr(), Hq * D, D
     else:
-        oa = _rows3(out, shape, dtype, "out")
+        oa = _rows3(dev, out, shape, dtype, "out")
     lse = _new((T, Hq), torch.float32, q, stream) if return_lse else None
     L = lib()
     need = L.lowbit_attention_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window)
     size = 0
     if workspace is not None:
         size = _given_workspace(workspace, need, "lowbit_attention")
+        if workspace.get_device() != dev:
+            raise _same_device(dev, workspace=workspace)
     elif need:
         workspace, size = _new(need, torch.uint8, q, stream), need
     _check(L.lowbit_attention(cache.ref, *head, T, max_tokens, max_len, _DT[dtype], *qa, Hq, *oa, _ptr(lse),
                               D ** -0.5 if scale is None else scale, causal, window, _ptr(workspace), size,
-                              _queue(stream, q.get_device())), "lowbit_attention")
+                              _queue(stream, dev)), "lowbit_attention")
     return (out, lse) if return_lse else out

@@ -240,3 +240,108 @@ def test_a_workspace_is_one_dense_block(b):
             b._given_workspace(t, 4096, "a call")
     with pytest.raises(ValueError, match="GPU"):
         b._given_workspace(torch.empty(4096, dtype=torch.uint8), 4096, "a call")
+
+
+# ------------------------------------------------------------------- devices ---
+
+class On(torch.Tensor):
+    """A host tensor that says it is on GPU `gpu` (the checks go by get_device)."""
+
+    def get_device(self):
+        return self.gpu
+
+
+def _on(gpu, shape, dtype):
+    t = torch.zeros(shape, dtype=dtype).as_subclass(On)
+    t.gpu = gpu
+    return t
+
+
+class Library:
+    """Stands in for the library: notes the device that is current in each call."""
+
+    def __init__(self, log):
+        self.log = log
+
+    def __getattr__(self, name):
+        return lambda *args: self.log.append((name, self.now, args)) or 0
+
+
+@pytest.fixture
+def two_gpus(b, monkeypatch):
+    lib = Library([])
+    lib.now = 0
+
+    class Device:
+        def __init__(self, index):
+            self.index = index
+
+        def __enter__(self):
+            self.was, lib.now = lib.now, self.index
+
+        def __exit__(self, *exc):
+            lib.now = self.was
+
+    monkeypatch.setattr(b, "lib", lambda: lib)
+    monkeypatch.setattr(b, "_new", lambda shape, dtype, like, stream: _on(like.gpu, shape, dtype))
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: lib.now, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 1000 + d, raising=False)
+    return lib
+
+
+def _operands(gpu, **other):
+    """Calls of the four operators with every operand on `gpu`, but those named in `other`."""
+    def t(name, shape, dtype):
+        return _on(other.get(name, gpu), shape, dtype)
+    i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
+
+    def cache(b):
+        return b.KVCache(t("k_cache", (3, 2, 16, 64), torch.uint8), t("v_cache", (3, 2, 16, 64), torch.uint8),
+                         t("k_scale", (3, 2), f32), t("v_scale", (3, 2), f32))
+
+    def where():
+        return t("block_table", (1, 3), i32), t("cu", (2,), i32), t("starts", (1,), i32)
+
+    rows = lambda n, h=2: t(n, (4, h, 64), bf)  # noqa: E731
+    return dict(
+        gemv=lambda b: b.gemv_int4(t("x", (2, 128), bf), t("packed", (8, 64), torch.uint8), t("scales", (8, 1), torch.float16),
+                                   t("zeros", (8, 1), torch.float16), bias=t("bias", (8,), f32), out=t("out", (2, 8), bf)),
+        append=lambda b: b.kv_append(rows("k"), rows("v"), cache(b), *where(), 4, q=rows("q", 4), cos=t("cos", (48, 32), f32),
+                                     sin=t("sin", (48, 32), f32), q_out=rows("q_out", 4), bad_count=t("bad", (2,), i32)),
+        read=lambda b: b.kv_read(cache(b), *where(), 4, 4, bf, out=(rows("k_out"), rows("v_out"))),
+        attend=lambda b: b.attention(rows("q", 4), cache(b), *where(), 4, 4, out=rows("out", 4), return_lse=True))
+
+
+@pytest.mark.parametrize("gpu", [0, 1])
+def test_calls_run_on_their_operands_device(b, two_gpus, gpu):
+    for call in _operands(gpu).values():
+        call(b)
+    made = {name: (device, args[-1]) for name, device, args in two_gpus.log}
+    assert {d for d, _ in made.values()} == {gpu} and two_gpus.now == 0 and len(made) == 5
+    assert all(q == 1000 + gpu for name, (_, q) in made.items() if "workspace" not in name)   # that device's current stream
+
+
+@pytest.mark.parametrize("call,names", [
+    ("gemv", ("x", "packed", "scales", "zeros", "bias", "out")),
+    ("append", ("k", "v", "k_cache", "v_cache", "k_scale", "v_scale", "block_table", "cu", "starts", "q", "cos", "sin",
+                "q_out", "bad")),
+    ("read", ("k_cache", "v_scale", "block_table", "cu", "starts", "k_out", "v_out")),
+    ("attend", ("q", "k_cache", "v_scale", "block_table", "cu", "starts", "out"))])
+def test_operands_of_another_device_are_refused(b, two_gpus, call, names):
+    for name in names:
+        for wrong in (1, -1):                                 # another GPU, the host
+            with pytest.raises(ValueError, match="must be on"):
+                _operands(0, **{name: wrong})[call](b)
+    with pytest.raises(ValueError, match="must be on a GPU"):
+        _operands(-1)[call](b)
+    assert not two_gpus.log
+
+
+def test_a_stream_of_another_device_is_refused(b, two_gpus):
+    class Stream:
+        device_index, cuda_stream = 1, 77
+
+    assert b._queue(Stream, 1) == 77
+    with pytest.raises(ValueError, match="stream"):
+        b._queue(Stream, 0)
