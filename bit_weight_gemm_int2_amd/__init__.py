@@ -552,9 +552,16 @@ class KVCache:
 
     k, v: uint8 [pages, kv_heads, page, head_dim], contiguous, in the block
     layout of include/lowbit.h; k_scale, v_scale: float32 [pages, kv_heads].
-    Made by new_kv_cache, filled by kv_append, read by attention and kv_read."""
+    Made by new_kv_cache, filled by kv_append, read by attention and kv_read.
+    It keeps the addresses of its tensors, so these are not assigned anew: a
+    larger cache is another KVCache."""
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "kv_heads", "page", "head_dim", "device", "struct", "ref")
+    __slots__ = ("_tensors", "kv_heads", "page", "head_dim", "device", "struct", "ref")
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         shape = k.shape
@@ -572,7 +579,7 @@ class KVCache:
         for t in (k, v, k_scale, v_scale):
             if not t.is_contiguous():
                 raise ValueError("k, v, k_scale and v_scale must be contiguous")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = (k, v, k_scale, v_scale)
         self.struct = _CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
                                    pages, heads, page, d)
         self.ref = ctypes.byref(self.struct)

@@ -338,6 +338,17 @@ def test_operands_of_another_device_are_refused(b, two_gpus, call, names):
     assert not two_gpus.log
 
 
+def test_a_cache_keeps_its_tensors(b, two_gpus):
+    """The calls go by the addresses taken when the cache was made: assigning a larger tensor would leave them behind."""
+    ts = [_on(0, shape, dt) for shape, dt in (((3, 2, 16, 64), torch.uint8),) * 2 + (((3, 2), torch.float32),) * 2]
+    cache = b.KVCache(*ts)
+    assert all(getattr(cache, n) is t for n, t in zip(("k", "v", "k_scale", "v_scale"), ts))
+    for n in ("k", "v", "k_scale", "v_scale"):
+        with pytest.raises(AttributeError):
+            setattr(cache, n, _on(0, (6, 2, 16, 64), torch.uint8))
+    assert cache.struct.k == ts[0].data_ptr() and cache.struct.v_scale == ts[3].data_ptr()
+
+
 def test_a_stream_of_another_device_is_refused(b, two_gpus):
     class Stream:
         device_index, cuda_stream = 1, 77
