@@ -730,6 +730,7 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a) {
   for (int k = 1; k < NG; ++k) v += acc[k][tid];
   v *= inverse_sum(l);
   const int64_t token = row / a.q_heads;
+  if (token < a.t.cu[0] || token >= a.t.cu[a.t.batch]) return;         // no sequence's: no part was written
   const int head = (int)(row % a.q_heads);
   *(u32x2*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) = u32x2{out2<BF16>(v[0], v[1]), out2<BF16>(v[2], v[3])};
   if (tid == 0) store_lse(a, token, head, m, l);

@@ -439,7 +439,9 @@ int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table,
  * them, so query i (from 0) is at position lens[b] - n + i. Token j is seen
  * when j < lens[b], j <= position (causal not 0), j > position - window
  * (window > 0), and its page exists. A query that sees nothing gives zeros
- * (and lse = -infinity).
+ * (and lse = -infinity); rows of no sequence (before cu_tokens[0] or from
+ * cu_tokens[batch] on, as in a batch padded to a fixed size) are not written,
+ * and a sequence's rows past max_tokens hold anything.
  * Scores, softmax and sums are FP32; queries enter the matrix product as FP16
  * after an exact scaling of each row by a power of two, codes exactly,
  * probabilities as FP16 relative to the row's largest p_j * v_scale: off by at

@@ -247,6 +247,27 @@ def test_attention_workspaces(lb):
             call(ws)
 
 
+@pytest.mark.parametrize("n,H,Hq", [(1, 2, 4), (100, 1, 2)])
+@pytest.mark.parametrize("L", [200, 3000])
+def test_attention_leaves_rows_of_no_sequence_alone(lb, n, H, Hq, L):
+    """Rows before and behind those that cu_tokens covers (a batch padded to a fixed
+    size) stay as they are, whether or not the context is split; a split's workspace
+    holds NaN beforehand."""
+    banner(f"attention, padded batch, {n} queries over {L}")
+    P = Paged([L], H, 16, 64, seed=104)
+    T = n + 12
+    q, _ = _values(np.random.default_rng(105), (T, Hq, 64), "bf16")
+    need = lb.lib().lowbit_attention_workspace_bytes(1, T, n, L, Hq, H, 64, 0)
+    assert (need > 0) == (L > 2000)
+    out = torch.full((T, Hq, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = torch.full((max(1, need // 4),), float("nan"), device="cuda")
+    cache, table, lens = P.cache(lb), _i32(P.table), _i32([L])
+    lb.attention(q, cache, table, _i32([5, 5 + n]), lens, n, L, out=out, workspace=ws)
+    want = lb.attention(q[5:5 + n], cache, table, _i32([0, n]), lens, n, L)
+    assert (out[:5] == 7).all() and (out[5 + n:] == 7).all()
+    assert torch.isfinite(want).all() and torch.allclose(out[5:5 + n].float(), want.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
