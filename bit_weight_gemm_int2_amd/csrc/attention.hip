@@ -680,7 +680,8 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a) {
   __shared__ float wt[CH], red[2][4];
   __shared__ __align__(16) f32x4 acc[NG][TPR];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t total = a.t.tokens * a.q_heads, row = blockIdx.x;
+  const int64_t total = a.t.tokens * a.q_heads, row = blockIdx.x + (int64_t)blockIdx.y * gridDim.x;
+  if (row >= total) return;
   const f32x2* ml = (const f32x2*)(a.part + a.splits * total * D);
   float m = NEG_INF;
   for (int s = tid; s < a.splits; s += 256) m = fmaxf(m, ml[s * total + row][0]);
@@ -756,8 +757,10 @@ hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
     launch_many<BF16, D, 4>(a, rows, st);
   else if constexpr (D == 128)
     launch_many<BF16, D, 8>(a, rows, st);
-  if (a.splits > 1)
-    attend_join_kernel<BF16, D><<<dim3((unsigned)(a.t.tokens * a.q_heads)), 256, 0, st>>>(a);
+  if (a.splits > 1) {
+    const int64_t total = a.t.tokens * a.q_heads, nx = std::min<int64_t>(total, 1 << 22);   // nx * 256 threads fit 32 bits
+    attend_join_kernel<BF16, D><<<dim3((unsigned)nx, (unsigned)((total + nx - 1) / nx)), 256, 0, st>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -268,6 +268,22 @@ def test_attention_leaves_rows_of_no_sequence_alone(lb, n, H, Hq, L):
     assert torch.isfinite(want).all() and torch.allclose(out[5:5 + n].float(), want.float(), rtol=2.0 ** -7, atol=2.0 ** -7)
 
 
+def test_attention_joins_more_rows_than_one_grid_dimension_holds(lb):
+    """65535 sequences of 260 heads, 17 million rows (a launch's first dimension holds
+    2^24 workgroups of 256 threads), split by a bound of 5000 tokens: all see the same
+    three tokens and ask the same."""
+    banner("attention: 17 million rows in two parts")
+    B, H, Hq, D = 65535, 4, 260, 64
+    P = Paged([3], H, 16, D, seed=106)
+    cache, one = P.cache(lb), _values(np.random.default_rng(107), (1, Hq, D), "f16")[0]
+    want = lb.attention(one, cache, _i32(P.table), _i32([0, 1]), _i32([3]), 1, 3)
+    table = _i32(P.table).expand(B, 1).contiguous()
+    assert lb.lib().lowbit_attention_workspace_bytes(B, B, 1, 5000, Hq, H, D, 0) == 2 * B * Hq * (D + 2) * 4
+    out = lb.attention(one.expand(B, Hq, D), cache, table, torch.arange(B + 1, dtype=torch.int32, device="cuda"),
+                       torch.full((B,), 3, dtype=torch.int32, device="cuda"), 1, 5000)
+    assert torch.equal(out, want.expand(B, Hq, D))
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
