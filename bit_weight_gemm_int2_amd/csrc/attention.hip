@@ -180,10 +180,10 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t token, int 
 // Bound by reading the cache where the GPU is full, by the conversion and the
 // waves' latency (about 40 GB/s a CU, with 4, 8 or 16 waves alike) where not.
 // Four waves walk 32-token steps of the part in turn, each with its own
-// running maximum, and meet in LDS at the end. A
-// wave reads its keys and values straight into registers (16 bytes a lane,
-// whole kilobytes a wave); the next step's loads are in flight while one is
-// computed.
+// running maximum, and meet in LDS at the end. A wave reads its keys and values
+// straight into registers (16 bytes a lane, whole kilobytes a wave); the next
+// step's loads are in flight while one is computed. One token of 32 sequences
+// over up to 8192 cached: 65 us, 4.7 TB/s.
 // ---------------------------------------------------------------------------
 // ONCE: one row tile a sequence and head, so the cache is read once, past the
 // L2 (two sequences of 131072 tokens: 79 us against 90; with three row tiles
@@ -392,11 +392,12 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows (prompts): 128 rows a workgroup (32 a wave), tiles of 64 tokens,
-// v_mfma_f32_32x32x16_f16. Bound by the matrix and vector instructions.
-// Codes go global -> registers one tile ahead, are converted to FP16 once per
-// workgroup and written to the other of two LDS stages in the order of the
-// MFMA operands (16 consecutive bytes a lane both ways).
+// Many rows (prompts): 128 or 256 rows a workgroup (32 a wave), tiles of 64
+// tokens, v_mfma_f32_32x32x16_f16. Bound by the matrix and vector instructions
+// (4096 queries over 20000 tokens: 1140 to 1190 us, 1.01 to 1.06 PFLOP/s).
+// Codes go global -> registers two tiles ahead, are converted to FP16 once per
+// workgroup one tile ahead and written to the other of two LDS stages in the
+// order of the MFMA operands (16 consecutive bytes a lane both ways).
 // ---------------------------------------------------------------------------
 namespace many {
 constexpr int TOK = 64;
@@ -435,10 +436,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int hh = lane >> 5, r = lane & 31;
-  // Later row tiles see more of the context: those of every sequence start
-  // first. Workgroups go to the XCDs in turn, so with 8 heads an XCD keeps one
-  // head's keys and values; the sequences rotate so that with fewer heads no
-  // XCD is left with the short ones.
   // Workgroups go to the XCDs in turn, so with 8 heads an XCD keeps one head's
   // keys and values. Later row tiles see more of the context: the first
   // sequence begins with them, the next one ends with them, and so on.
@@ -806,10 +803,13 @@ AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens,
     n = std::max(n, fill);
     len = std::min<int64_t>((span + n - 1) / n, FEW_SPLIT);
   } else {
-    // 256 rows a workgroup halve the conversion of codes per row (4096 queries
-    // over 20000 tokens: 1147 us against 1234) but leave one workgroup a CU:
-    // only where tiles are many and long (2000 queries over 2000 tokens: 63
-    // against 55)
+    // 256 rows a workgroup halve the conversion of codes per row but leave one
+    // workgroup a CU: only where its tiles are long and fill two rounds (32
+    // query heads, 4000 queries over 20000 tokens, 504 tiles: 1127 us against
+    // 1217 with 128 rows; 5000, 632 tiles: 1539 against 1491; 3000, 376 tiles:
+    // 1045 against 970; one round would do as well, 2000, 250 tiles: 616
+    // against 660; shorter contexts gain nothing, two of 4000 over 5000: 330
+    // against 332)
     p.waves = D == 128 && span >= 8192 && batch * heads * ((rows + 255) / 256) >= 2 * num_cu ? 8 : 4;
     const int64_t tiles = batch * heads * ((rows + 32 * p.waves - 1) / (32 * p.waves));
     n = std::max<int64_t>(1, std::min((int64_t)8 * num_cu / p.waves / std::max<int64_t>(tiles, 1), span / 1024));
