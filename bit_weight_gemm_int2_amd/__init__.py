@@ -150,11 +150,12 @@ def new_workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
 
 def _given_workspace(workspace: torch.Tensor, need: int, what: str) -> int:
     """The bytes of a workspace given by the caller: one dense block of GPU
-    memory (the elements of an expanded or strided tensor count more bytes
-    than it owns, or others than those behind its address)."""
-    if not workspace.is_contiguous():
+    memory where one is needed (the elements of an expanded or strided tensor
+    count more bytes than it owns, or others than those behind its address)."""
+    if need and not workspace.is_contiguous():
         raise ValueError("workspace must be contiguous")
-    _cuda(workspace, "workspace")
+    if need:
+        _cuda(workspace, "workspace")
     size = workspace.numel() * workspace.element_size()
     if size < need:
         raise ValueError(f"workspace holds {size} bytes, {what} needs {need}")
@@ -554,7 +555,7 @@ class KVCache:
     layout of include/lowbit.h; k_scale, v_scale: float32 [pages, kv_heads].
     Made by new_kv_cache, filled by kv_append, read by attention and kv_read.
     It keeps the addresses of its tensors, so these are not assigned anew: a
-    larger cache is another KVCache."""
+    larger cache is another KVCache. device: the number of their GPU."""
 
     __slots__ = ("_tensors", "kv_heads", "page", "head_dim", "device", "struct", "ref")
 
