@@ -284,6 +284,32 @@ def test_attention_joins_more_rows_than_one_grid_dimension_holds(lb):
     assert torch.equal(out, want.expand(B, Hq, D))
 
 
+@pytest.mark.parametrize("new", [[1, 1], [50, 70]])
+def test_head_major_operands_give_the_same_bits(lb, new):
+    """Every dense operand as [heads, tokens, head_dim] in memory, queries, keys and
+    values in one block, against the token-major layout."""
+    banner(f"head-major operands, {new} new tokens")
+    H, Hq, D, page, past = 2, 6, 128, 32, [37, 100]
+    lens = [p + n for p, n in zip(past, new)]
+    P, T = Paged(lens, H, page, D, seed=108), sum(new)
+    x, _ = _values(np.random.default_rng(109), (T, Hq + 2 * H, D), "bf16")
+    cos, sin = (torch.from_numpy(a).cuda() for a in _rope(max(lens), D))
+    at = (_i32(P.table), _i32([0, new[0], T]))
+    res = []
+    for swap in (False, True):
+        order = (lambda t: t.transpose(0, 1).contiguous().transpose(0, 1)) if swap else (lambda t: t)
+        y, cache = order(x), P.cache(lb)
+        out = [order(torch.full((T, h, D), 7.0, dtype=x.dtype, device="cuda")) for h in (Hq, Hq, H, H)]
+        q = lb.kv_append(y[:, Hq:Hq + H], y[:, Hq + H:], cache, *at, _i32(past), max(new), q=y[:, :Hq], cos=cos, sin=sin,
+                         q_out=out[0])
+        o = lb.attention(q, cache, *at, _i32(lens), max(new), max(lens), out=out[1])
+        k, v = lb.kv_read(cache, *at, _i32(past), T, max(new), out=(out[2], out[3]))
+        assert q is out[0] and o is out[1] and q.is_contiguous() != swap
+        res.append([q, o, k, v, cache.k, cache.v, cache.k_scale, cache.v_scale])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
 # -------------------------------------- the many-row kernel (over 80 rows a head) ---
 
 def _parts(lb, lens, new, H, Hq, D, window=0):
