@@ -12,7 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -28,6 +28,7 @@ GROUP = 128
 _FMT = {"ternary": TERNARY, "binary": BINARY, "base3": BASE3, "int4": INT4, TERNARY: TERNARY, BINARY: BINARY,
         BASE3: BASE3, INT4: INT4}
 _DT = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
+_ROPE = {None: 0, "linear": 1, "ntk": 2, "yarn": 3, "wavelength": 4}
 _ACT = {None: ACT_NONE, "none": ACT_NONE, "gelu": ACT_GELU, ACT_NONE: ACT_NONE, ACT_GELU: ACT_GELU}
 
 _lib = None
@@ -67,6 +68,20 @@ SIGNATURES = [
     ("lowbit_attention", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64,
                                 _P, _I64, _I64, _P, ctypes.c_float, _I32, _I64, _P, _SZ, _P]),
     ("lowbit_attention_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64]),
+    ("lowbit_kv_append_norm", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I32, _P, _I64, _I64, _P, _I64, _I64,
+                                     _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _P, _I64, _I64, _I32, _P, _P, _I32,
+                                     ctypes.c_float, _P, _P]),
+    ("lowbit_norm_rotate", _I32, [_I32, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _I64, _P, _I64,
+                                  _I64, _P, _P, _I32, ctypes.c_float, _P, _P, _I64, _I64, _P, _I32, _P, _P]),
+    ("lowbit_rope_tables", _I32, [_P, _P, _I64, _I64, _I64, ctypes.c_double, _I32] + [ctypes.c_double] * 5 + [_P]),
+    ("lowbit_kv_remap", _I32, [_P, _I64, _P, _I64, _I64, _I32, _P, _P, _I64, _I64, _I64, _I32, _P, _I64, _P, _P, _P, _I64,
+                               _P, _P, _SZ, _P]),
+    ("lowbit_kv_remap_pairs", _I64, [_I64, _I64, _I64, _I32]),
+    ("lowbit_kv_remap_workspace_bytes", _SZ, [_I64, _I64]),
+    ("lowbit_kv_copy_pages", _I32, [_P, _P, _P, _I64, _P, _P]),
+    ("lowbit_attention_sinks", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64,
+                                      _P, _I64, _I64, _P, ctypes.c_float, _I32, _I64, _I64, _P, _SZ, _P]),
+    ("lowbit_attention_sinks_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64]),
     ("lowbit_quantize", _I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
 ]
 MAX_GROUP = 8
@@ -451,8 +466,8 @@ def gelu(x: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> to
 
 
 # ---------------------------------------------------------------------------
-# Decoding: 4-bit products of a few rows, the 8-bit paged key/value cache and
-# attention over it
+# Decoding: 4-bit products of a few rows, the 8-bit paged key/value cache, its
+# pages, norms and rotation of queries and keys, and attention over the cache
 # ---------------------------------------------------------------------------
 
 def _queue(stream, device: int) -> int:
@@ -617,19 +632,62 @@ def _rows3(dev: int, t: torch.Tensor, shape, dtype, name: str):
     return t.data_ptr(), ts, hs
 
 
+def _turns(dev: int, cos, sin):
+    """(positions, rot) of the rotation's tables, checked; (0, 0) without them."""
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is None:
+        return 0, 0
+    if cos.dim() != 2 or sin.shape != cos.shape:
+        raise ValueError("cos and sin must be [positions, rot/2]")
+    for t in (cos, sin):
+        if t.get_device() != dev:
+            raise _same_device(dev, cos=cos, sin=sin)
+        if t.dtype != torch.float32 or not t.is_contiguous():
+            raise ValueError("cos and sin must be contiguous float32 tensors")
+    positions, half = cos.shape
+    return positions, 2 * half
+
+
+def _counter(dev: int, bad_count, n: int):
+    if bad_count is not None:
+        if bad_count.get_device() != dev:
+            raise _same_device(dev, bad_count=bad_count)
+        if bad_count.dtype != torch.int32 or bad_count.numel() != n or not bad_count.is_contiguous():
+            raise ValueError(f"bad_count must be int32 [{n}]")
+
+
+def _norms(dev: int, D: int, q_norm, k_norm) -> int:
+    """The type of the norms' weights, checked."""
+    dtype = None
+    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if t is None:
+            continue
+        if t.get_device() != dev:
+            raise _same_device(dev, **{name: t})
+        if t.shape != (D,) or t.dtype not in _DT or not t.is_contiguous() or t.dtype != (dtype or t.dtype):
+            raise ValueError(f"q_norm and k_norm must be contiguous float16, bfloat16 or float32 [{D}] of one type")
+        dtype = t.dtype
+    return NONE if dtype is None else _DT[dtype]
+
+
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor,
               starts: torch.Tensor, max_tokens: int, q: Optional[torch.Tensor] = None,
               cos: Optional[torch.Tensor] = None, sin: Optional[torch.Tensor] = None, interleaved: bool = False,
-              q_out: Optional[torch.Tensor] = None, bad_count: Optional[torch.Tensor] = None, stream=None):
+              q_out: Optional[torch.Tensor] = None, bad_count: Optional[torch.Tensor] = None, stream=None,
+              q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, eps: float = 1e-6):
     """Append new keys and values to the cache, rotated by position on the
-    way (lowbit_kv_append); returns the rotated queries when q is given.
+    way (lowbit_kv_append, lowbit_kv_append_norm); returns the rotated queries
+    when q is given.
 
     k, v: [T, kv_heads, head_dim] and q: [T, q_heads, head_dim] of one dtype
     (fp16, bf16, fp32), last dimension contiguous (slices of a fused
     projection's output do). Sequence b's rows are cu_tokens[b] ..
     cu_tokens[b+1] - 1 and go to positions starts[b], ...; max_tokens is a
     host bound on the rows of one sequence. cos, sin: float32 [positions,
-    rot/2], both or none. bad_count: int32 [2], added to: non-finite values
+    rot/2], both or none (rope_tables makes them). q_norm, k_norm: weights
+    [head_dim] of one dtype for the norm of each head before the rotation,
+    x / sqrt(mean x^2 + eps) * w. bad_count: int32 [2], added to: non-finite values
     (stored as 0) and tokens left out (no page or no position; a query
     without a position comes back as zeros)."""
     if k.dim() != 3:
@@ -644,7 +702,7 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
     if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
         with torch.cuda.device(dev):
             return kv_append(k, v, cache, block_table, cu_tokens, starts, max_tokens, q, cos, sin, interleaved, q_out,
-                             bad_count, stream)
+                             bad_count, stream, q_norm, k_norm, eps)
     head = _table(dev, block_table, cu_tokens, starts, "starts")
     ka, va = _rows3(dev, k, shape, dtype, "k"), _rows3(dev, v, shape, dtype, "v")
     if q is not None:
@@ -659,24 +717,16 @@ def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: tor
         if q_out is not None:
             raise ValueError("q_out without q")
         Hq, qa, qo = 0, (None, 0, 0), (None, 0, 0)
-    rot = positions = 0
-    if (cos is None) != (sin is None):
-        raise ValueError("cos and sin go together")
-    if cos is not None:
-        if cos.dim() != 2 or sin.shape != cos.shape:
-            raise ValueError("cos and sin must be [positions, rot/2]")
-        for t in (cos, sin):
-            if t.get_device() != dev:
-                raise _same_device(dev, cos=cos, sin=sin)
-            if t.dtype != torch.float32 or not t.is_contiguous():
-                raise ValueError("cos and sin must be contiguous float32 tensors")
-        positions, rot = cos.shape
-        rot *= 2
-    if bad_count is not None:
-        if bad_count.get_device() != dev:
-            raise _same_device(dev, bad_count=bad_count)
-        if bad_count.dtype != torch.int32 or bad_count.numel() != 2 or not bad_count.is_contiguous():
-            raise ValueError("bad_count must be int32 [2]")
+    positions, rot = _turns(dev, cos, sin)
+    _counter(dev, bad_count, 2)
+    if q_norm is not None or k_norm is not None:
+        if q_norm is not None and q is None:
+            raise ValueError("q_norm without q")
+        ndt = _norms(dev, D, q_norm, k_norm)
+        _check(lib().lowbit_kv_append_norm(cache.ref, *head, T, max_tokens, _DT[dtype], *ka, *va, *qa, Hq, *qo, _ptr(cos),
+                                           _ptr(sin), rot, positions, interleaved, _ptr(q_norm), _ptr(k_norm), ndt, eps,
+                                           _ptr(bad_count), _queue(stream, dev)), "lowbit_kv_append_norm")
+        return q_out
     _check(lib().lowbit_kv_append(cache.ref, *head, T, max_tokens, _DT[dtype], *ka, *va, *qa, Hq, *qo, _ptr(cos),
                                   _ptr(sin), rot, positions, interleaved, _ptr(bad_count),
                                   _queue(stream, dev)), "lowbit_kv_append")
@@ -713,15 +763,17 @@ def kv_read(cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor, 
 def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor,
               lens: torch.Tensor, max_tokens: int, max_len: int, scale: Optional[float] = None, causal: bool = True,
               window: int = 0, out: Optional[torch.Tensor] = None, return_lse: bool = False,
-              workspace: Optional[torch.Tensor] = None, stream=None):
-    """Attention of new queries over the cache (lowbit_attention).
+              workspace: Optional[torch.Tensor] = None, stream=None, sinks: int = 0):
+    """Attention of new queries over the cache (lowbit_attention,
+    lowbit_attention_sinks).
 
     q: [T, q_heads, head_dim] fp16/bf16, last dimension contiguous; q_heads a
     multiple of the cache's heads. Sequence b has lens[b] tokens in the cache
     and its queries are rows cu_tokens[b] .. cu_tokens[b+1] - 1, the last ones
     of it. max_tokens and max_len are host bounds on the queries and the length
     of one sequence. scale defaults to head_dim ** -0.5; window > 0 keeps the
-    last `window` tokens of each query. Returns out, or (out, lse) with the
+    last `window` tokens of each query, and the first `sinks` of the sequence
+    beside them. Returns out, or (out, lse) with the
     float32 [T, q_heads] log of the softmax's sum."""
     dtype = q.dtype
     if q.dim() != 3 or (dtype != torch.bfloat16 and dtype != torch.float16):
@@ -735,7 +787,7 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
     if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
         with torch.cuda.device(dev):
             return attention(q, cache, block_table, cu_tokens, lens, max_tokens, max_len, scale, causal, window, out,
-                             return_lse, workspace, stream)
+                             return_lse, workspace, stream, sinks)
     head = _table(dev, block_table, cu_tokens, lens, "lens")
     qa = _rows3(dev, q, shape, dtype, "q")
     if out is None:
@@ -745,7 +797,10 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
         oa = _rows3(dev, out, shape, dtype, "out")
     lse = _new((T, Hq), torch.float32, q, stream) if return_lse else None
     L = lib()
-    need = L.lowbit_attention_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window)
+    if sinks:
+        need = L.lowbit_attention_sinks_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window, sinks)
+    else:
+        need = L.lowbit_attention_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window)
     size = 0
     if workspace is not None:
         size = _given_workspace(workspace, need, "lowbit_attention")
@@ -753,7 +808,215 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
             raise _same_device(dev, workspace=workspace)
     elif need:
         workspace, size = _new(need, torch.uint8, q, stream), need
-    _check(L.lowbit_attention(cache.ref, *head, T, max_tokens, max_len, _DT[dtype], *qa, Hq, *oa, _ptr(lse),
-                              D ** -0.5 if scale is None else scale, causal, window, _ptr(workspace), size,
-                              _queue(stream, dev)), "lowbit_attention")
+    scale = D ** -0.5 if scale is None else scale
+    if sinks:
+        _check(L.lowbit_attention_sinks(cache.ref, *head, T, max_tokens, max_len, _DT[dtype], *qa, Hq, *oa, _ptr(lse),
+                                        scale, causal, window, sinks, _ptr(workspace), size, _queue(stream, dev)),
+               "lowbit_attention_sinks")
+    else:
+        _check(L.lowbit_attention(cache.ref, *head, T, max_tokens, max_len, _DT[dtype], *qa, Hq, *oa, _ptr(lse),
+                                  scale, causal, window, _ptr(workspace), size, _queue(stream, dev)), "lowbit_attention")
     return (out, lse) if return_lse else out
+
+
+def norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor] = None, q_norm: Optional[torch.Tensor] = None,
+                k_norm: Optional[torch.Tensor] = None, cos: Optional[torch.Tensor] = None,
+                sin: Optional[torch.Tensor] = None, positions: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                interleaved: bool = False, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                bad_count: Optional[torch.Tensor] = None, stream=None):
+    """The norm of each head of dense queries and keys and their rotation by
+    position, in one pass (lowbit_norm_rotate). Returns q_out, or (q_out,
+    k_out) when k is given.
+
+    q: [T, q_heads, head_dim], k: [T, k_heads, head_dim] of one dtype (fp16,
+    bf16, fp32), last dimension contiguous. q_norm, k_norm: weights [head_dim]
+    of one dtype, each optional. cos, sin: float32 [rows, rot/2], both or none;
+    token t takes row positions[t] (int32 [T]), or row t. bad_count: int32 [1],
+    added to: tokens without a row, which become zeros. q_out may be q, k_out
+    may be k."""
+    if q.dim() != 3 or q.dtype not in _DT:
+        raise ValueError("q must be float16, bfloat16 or float32 [tokens, heads, head_dim]")
+    dtype, dev = q.dtype, q.get_device()
+    T, Hq, D = q.shape
+    if dev < 0:
+        raise _same_device(dev, q=q)
+    if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
+        with torch.cuda.device(dev):
+            return norm_rotate(q, k, q_norm, k_norm, cos, sin, positions, eps, interleaved, q_out, k_out, bad_count, stream)
+    qa = _rows3(dev, q, (T, Hq, D), dtype, "q")
+    if q_out is None:
+        q_out = _new((T, Hq, D), dtype, q, stream)
+        qo = q_out.data_ptr(), Hq * D, D
+    else:
+        qo = _rows3(dev, q_out, (T, Hq, D), dtype, "q_out")
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must be [tokens, heads, head_dim]")
+        Hk = k.shape[1]
+        ka = _rows3(dev, k, (T, Hk, D), dtype, "k")
+        if k_out is None:
+            k_out = _new((T, Hk, D), dtype, q, stream)
+            ko = k_out.data_ptr(), Hk * D, D
+        else:
+            ko = _rows3(dev, k_out, (T, Hk, D), dtype, "k_out")
+    else:
+        if k_out is not None or k_norm is not None:
+            raise ValueError("k_out or k_norm without k")
+        Hk, ka, ko = 0, (None, 0, 0), (None, 0, 0)
+    rows, rot = _turns(dev, cos, sin)
+    if positions is not None:
+        if positions.get_device() != dev:
+            raise _same_device(dev, positions=positions)
+        if not rot:
+            raise ValueError("positions without cos and sin")
+        if positions.shape != (T,) or positions.dtype != torch.int32 or not positions.is_contiguous():
+            raise ValueError(f"positions must be contiguous int32 [{T}]")
+    _counter(dev, bad_count, 1)
+    if not rot and q_norm is None and k_norm is None:
+        raise ValueError("neither a norm nor a rotation")
+    ndt = _norms(dev, D, q_norm, k_norm)
+    _check(lib().lowbit_norm_rotate(_DT[dtype], T, D, *qa, Hq, *qo, *ka, Hk, *ko, _ptr(q_norm), _ptr(k_norm), ndt, eps,
+                                    _ptr(cos), _ptr(sin), rot, rows, _ptr(positions), interleaved, _ptr(bad_count),
+                                    _queue(stream, dev)), "lowbit_norm_rotate")
+    return q_out if k is None else (q_out, k_out)
+
+
+def rope_tables(positions: int, rot: int, base: float = 1e4, scaling: Optional[str] = None, factor: float = 1.0,
+                original: float = 0.0, low: float = 1.0, high: float = 32.0, magnitude: Optional[float] = None, first: int = 0,
+                device=None, out=None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """cos and sin (float32 [positions, rot/2]) of the positions first, first +
+    1, ... for kv_append and norm_rotate (lowbit_rope_tables).
+
+    scaling: None, or for contexts longer than the `original` length "linear"
+    (positions divided by factor), "ntk" (a larger base), "yarn" (frequencies
+    divided by factor where they make few turns over the original length, all
+    of it under `low` and none over `high`, in steps by dimension) or
+    "wavelength" (the same by turns). magnitude: of the entries; None for the
+    rule's own (0.1 log(factor) + 1 with "yarn", else 1). out = (cos, sin) to
+    write into."""
+    if scaling not in _ROPE:
+        raise ValueError(f"scaling must be None, 'linear', 'ntk', 'yarn' or 'wavelength', not {scaling!r}")
+    shape = (positions, rot // 2)
+    if out is None:
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            raise ValueError("the tables must be on a GPU")
+        index = torch._C._cuda_getDevice() if dev.index is None else dev.index
+    else:
+        cos, sin = out
+        index = cos.get_device()
+        if index < 0 or sin.get_device() != index:
+            raise _same_device(index, sin=sin)
+        for t in out:
+            if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError(f"cos and sin must be contiguous float32 {list(shape)}")
+    if torch._C._cuda_getDevice() != index:   # the library launches for the current device
+        with torch.cuda.device(index):
+            return rope_tables(positions, rot, base, scaling, factor, original, low, high, magnitude, first,
+                               torch.device("cuda", index), out, stream)
+    if out is None:
+        with torch.cuda.stream(stream):       # no stream given: the current one
+            cos, sin = (torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", index)) for _ in range(2))
+    _check(lib().lowbit_rope_tables(cos.data_ptr(), sin.data_ptr(), positions, rot, first, base, _ROPE[scaling], factor,
+                                    original, low, high, 0.0 if magnitude is None else magnitude, _queue(stream, index)),
+           "lowbit_rope_tables")
+    return cos, sin
+
+
+class PagePlan(NamedTuple):
+    """What kv_remap returns: the new table and lengths, the pages to copy in
+    every layer's cache (kv_copy_pages(cache, plan.src, plan.dst,
+    plan.counts)), and counts: pairs, pages in use afterwards, slots that found
+    no page, moves among the pairs."""
+    table: torch.Tensor
+    lens: torch.Tensor
+    src: torch.Tensor
+    dst: torch.Tensor
+    counts: torch.Tensor
+
+
+def kv_remap(block_table: torch.Tensor, lens: torch.Tensor, cache: KVCache, rows: Optional[torch.Tensor] = None,
+             room: Optional[torch.Tensor] = None, window: int = 0, sinks: int = 0, compact: bool = False,
+             width: Optional[int] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> PagePlan:
+    """A new table of pages for the sequences that go on (lowbit_kv_remap),
+    without waiting for the GPU.
+
+    block_table: int32 [batch, pages of a sequence], lens: int32 [batch] tokens
+    in the cache. rows: int32 [new batch], the old sequence that each new one
+    continues (default: each itself; twice the same forks it, one that is not
+    named ends, a number that is none begins an empty one). room: int32 [new
+    batch], tokens that each new sequence needs pages for beside those it has.
+    window, sinks: pages that attention with these will not read again are let
+    go. compact: the pages in use move to the front of the pool. width: pages
+    of a sequence in the new table (default: as before). Copy what plan.src and
+    plan.dst name in every layer's cache before the next append."""
+    dev = cache.device
+    if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
+        with torch.cuda.device(dev):
+            return kv_remap(block_table, lens, cache, rows, room, window, sinks, compact, width, workspace, stream)
+    named = dict(block_table=block_table, lens=lens)
+    if rows is not None:
+        named["rows"] = rows
+    if room is not None:
+        named["room"] = room
+    for t in named.values():
+        if t.get_device() != dev:
+            raise _same_device(dev, **named)
+        if t.dtype != torch.int32 or not t.is_contiguous():
+            raise ValueError("block_table, lens, rows and room must be contiguous int32 tensors")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be a contiguous int32 tensor [batch, pages of a sequence]")
+    batch, old = block_table.shape
+    if lens.shape != (batch,):
+        raise ValueError(f"lens must be int32 [{batch}]")
+    if rows is not None and rows.dim() != 1:
+        raise ValueError("rows must be one-dimensional")
+    n = batch if rows is None else rows.shape[0]
+    if room is not None and room.shape != (n,):
+        raise ValueError(f"room must be int32 [{n}]")
+    wide = old if width is None else width
+    pages, L = cache.struct.pages, lib()
+    pairs = L.lowbit_kv_remap_pairs(old, n, pages, compact)
+    need = L.lowbit_kv_remap_workspace_bytes(n, pages)
+    if pairs < 0 or wide < 0 or not need:
+        raise LowbitError(ERR_SHAPE, "lowbit_kv_remap")
+    size = need
+    if workspace is None:
+        workspace = _new(need, torch.uint8, block_table, stream)
+    else:
+        size = _given_workspace(workspace, need, "lowbit_kv_remap")
+        if workspace.get_device() != dev:
+            raise _same_device(dev, workspace=workspace)
+    made = _new(n * wide + n + 2 * pairs + 4, torch.int32, block_table, stream)
+    table, new_lens, src, dst, counts = made.split((n * wide, n, pairs, pairs, 4))
+    plan = PagePlan(table.view(n, wide), new_lens, src, dst, counts)
+    _check(L.lowbit_kv_remap(block_table.data_ptr(), old, lens.data_ptr(), batch, pages, cache.page, _ptr(rows), _ptr(room), n,
+                             window, sinks, compact, table.data_ptr(), wide, new_lens.data_ptr(), src.data_ptr(),
+                             dst.data_ptr(), pairs, counts.data_ptr(), workspace.data_ptr(), size, _queue(stream, dev)),
+           "lowbit_kv_remap")
+    return plan
+
+
+def kv_copy_pages(cache: KVCache, src: torch.Tensor, dst: torch.Tensor, count: Optional[torch.Tensor] = None, stream=None):
+    """Copy pages inside the cache: page dst[i] becomes page src[i]
+    (lowbit_kv_copy_pages), for the first count[0] pairs where count is given.
+
+    src, dst: int32 [pairs]; pairs with a number that is no page are left out.
+    count: int32, its first element counts (PagePlan.counts). No page may be the
+    destination of two sources, or a source and a destination."""
+    dev = cache.device
+    if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
+        with torch.cuda.device(dev):
+            return kv_copy_pages(cache, src, dst, count, stream)
+    if not dev == src.get_device() == dst.get_device():
+        raise _same_device(dev, src=src, dst=dst)
+    for t in (src, dst):
+        if t.dim() != 1 or t.dtype != torch.int32 or not t.is_contiguous() or t.shape != src.shape:
+            raise ValueError("src and dst must be contiguous int32 [pairs] of one length")
+    if count is not None:
+        if count.get_device() != dev:
+            raise _same_device(dev, count=count)
+        if count.dtype != torch.int32 or not count.numel() or not count.is_contiguous():
+            raise ValueError("count must be a contiguous int32 tensor of one element or more")
+    _check(lib().lowbit_kv_copy_pages(cache.ref, src.data_ptr(), dst.data_ptr(), src.shape[0], _ptr(count),
+                                      _queue(stream, dev)), "lowbit_kv_copy_pages")

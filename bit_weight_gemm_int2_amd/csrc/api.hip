@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdlib>
 #include <algorithm>
 #include <cstring>
@@ -13,6 +14,7 @@
 #include "../../include/lowbit.h"
 #include "common.h"
 #include "kvcache.h"
+#include "pages.h"
 
 namespace lowbit {
 hipError_t launch_pack(int fmt, const int8_t* codes, int64_t N, int64_t K, uint8_t* packed,
@@ -31,8 +33,14 @@ hipError_t launch_gemv_int4(bool x_bf16, const GemmArgs& a, int num_cu, hipStrea
 hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st);
 hipError_t launch_kv_read(const KvReadArgs& g, hipStream_t st);
 hipError_t launch_attention(const AttnArgs& a, AttnPlan p, hipStream_t st);
-AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
-                        int num_cu);
+AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
+                        int D, int num_cu);
+hipError_t launch_norm_rotate(const TurnArgs& g, hipStream_t st);
+hipError_t launch_rope_tables(const TableArgs& g, hipStream_t st);
+size_t remap_workspace(int64_t new_batch, int64_t pages);
+hipError_t launch_remap(RemapArgs g, void* workspace, int num_cu, hipStream_t st);
+hipError_t launch_copy_pages(const KvCache& c, const int32_t* src, const int32_t* dst, int pairs, const int32_t* count,
+                             int num_cu, hipStream_t st);
 int64_t int4_rows(int64_t M);
 size_t int4_workspace(int M, int N, int K, int num_cu, int variant);
 size_t small_workspace_bytes(int M, int N, int K, int num_cu, int variant, int count = 1);
@@ -620,6 +628,9 @@ bool any_overlap(Range a, std::initializer_list<Range> others) {
   return false;
 }
 
+bool page_size(int32_t page) { return page == 16 || page == 32 || page == 64 || page == 128 || page == 256; }
+bool head_size(int64_t d) { return d == 64 || d == 128 || d == 256; }
+
 // Checks shared by the calls on the paged cache.
 int32_t check_cache(const lowbit_kv_cache* c, const int32_t* table, int64_t width, const int32_t* cu,
                     const int32_t* start, int64_t batch, int64_t tokens, int64_t max_tokens) {
@@ -629,8 +640,7 @@ int32_t check_cache(const lowbit_kv_cache* c, const int32_t* table, int64_t widt
   if (c->pages < 1 || c->kv_heads < 1 || c->kv_heads > 4096 || c->pages >= kMaxDim ||
       c->pages * c->kv_heads >= kMaxDim)
     return LOWBIT_ERR_SHAPE;
-  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256) return LOWBIT_ERR_SHAPE;
-  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return LOWBIT_ERR_SHAPE;
+  if (!page_size(c->page) || !head_size(c->head_dim)) return LOWBIT_ERR_SHAPE;
   if (width < 0 || width >= kMaxDim || batch < 0 || batch > 65535 || tokens < 0 || tokens >= kMaxDim ||
       max_tokens < 0 || max_tokens >= ((int64_t)1 << 30) || (tokens && (batch < 1 || max_tokens < 1)))
     return LOWBIT_ERR_SHAPE;
@@ -688,16 +698,29 @@ lowbit::KvTable table_args(const int32_t* table, int64_t width, const int32_t* c
 
 int64_t cache_bytes(const lowbit_kv_cache* c) { return c->pages * c->kv_heads * c->page * (int64_t)c->head_dim; }
 
-}  // namespace
+// The weights of the heads' norms, as the calls that have them take them.
+struct Norms {
+  const void* q;
+  const void* k;
+  int32_t dtype;
+  float eps;
+  int64_t bytes(int64_t D) const { return D * (dtype == LOWBIT_F32 ? 4 : 2); }
+};
 
-extern "C" {
+int32_t check_norms(const Norms& n, bool queries) {
+  if (!n.q && !n.k) return n.dtype == LOWBIT_NONE ? LOWBIT_OK : LOWBIT_ERR_NULL;
+  if (n.dtype != LOWBIT_F16 && n.dtype != LOWBIT_BF16 && n.dtype != LOWBIT_F32) return LOWBIT_ERR_DTYPE;
+  if (n.q && !queries) return LOWBIT_ERR_NULL;
+  if (!(n.eps >= 0.0f) || !(n.eps <= 3.402823466e38f)) return LOWBIT_ERR_SHAPE;
+  return aligned(n.q, 16) && aligned(n.k, 16) ? LOWBIT_OK : LOWBIT_ERR_ALIGN;
+}
 
-int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
-                         const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
-                         int64_t max_tokens, int32_t dtype, const void* k, int64_t kts, int64_t khs, const void* v,
-                         int64_t vts, int64_t vhs, const void* q, int64_t qts, int64_t qhs, int64_t q_heads,
-                         void* q_out, int64_t ots, int64_t ohs, const float* cos, const float* sin, int64_t rot,
-                         int64_t rope_rows, int32_t interleaved, int32_t* bad_count, void* stream) {
+int32_t kv_append(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                  const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens, int64_t max_tokens,
+                  int32_t dtype, const void* k, int64_t kts, int64_t khs, const void* v, int64_t vts, int64_t vhs,
+                  const void* q, int64_t qts, int64_t qhs, int64_t q_heads, void* q_out, int64_t ots, int64_t ohs,
+                  const float* cos, const float* sin, int64_t rot, int64_t rope_rows, int32_t interleaved,
+                  const Norms& norms, int32_t* bad_count, void* stream) {
   if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16 && dtype != LOWBIT_F32) return LOWBIT_ERR_DTYPE;
   int32_t st = check_cache(cache, block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
   if (st) return st;
@@ -705,6 +728,7 @@ int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_tabl
   if (rot < 0 || rot > D || rot % 32 || (rot && (rope_rows < 1 || rope_rows >= kMaxDim))) return LOWBIT_ERR_SHAPE;
   if ((rot != 0) != (cos != nullptr) || (rot != 0) != (sin != nullptr)) return LOWBIT_ERR_NULL;
   if ((q == nullptr) != (q_out == nullptr)) return LOWBIT_ERR_NULL;
+  if ((st = check_norms(norms, q != nullptr))) return st;
   if (q && (q_heads < 1 || q_heads > 65536)) return LOWBIT_ERR_SHAPE;
   if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(bad_count, 4)) return LOWBIT_ERR_ALIGN;
   if (!tokens) return LOWBIT_OK;
@@ -718,14 +742,15 @@ int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_tabl
               ro = rows_range(q_out, ots, ohs, tokens, q_heads, D, dtype),
               tab{block_table, batch * table_width * 4}, cu{cu_tokens, (batch + 1) * 4}, sta{starts, batch * 4},
               co{cos, rope_rows * rot * 2}, si{sin, rope_rows * rot * 2}, ck{cache->k, cb}, cv{cache->v, cb},
-              ks{cache->k_scale, sb}, vs{cache->v_scale, sb}, bad{bad_count, 8};
+              ks{cache->k_scale, sb}, vs{cache->v_scale, sb}, bad{bad_count, 8}, qn{norms.q, norms.bytes(D)},
+              kn{norms.k, norms.bytes(D)};
   for (const Range& w : {ck, cv, ks, vs, bad})
-    if (any_overlap(w, {rk, rv, rq, tab, cu, sta, co, si})) return LOWBIT_ERR_OVERLAP;
+    if (any_overlap(w, {rk, rv, rq, tab, cu, sta, co, si, qn, kn})) return LOWBIT_ERR_OVERLAP;
   const bool in_place = q == q_out && qts == ots && qhs == ohs;
   const Rows to = rows_of(q_out, ots, ohs, tokens, q_heads, D, dtype);
   if ((!in_place && rows_overlap(to, rows_of(q, qts, qhs, tokens, q_heads, D, dtype))) ||
       rows_overlap(to, rows_of(k, kts, khs, tokens, H, D, dtype)) ||
-      rows_overlap(to, rows_of(v, vts, vhs, tokens, H, D, dtype)) || any_overlap(ro, {tab, cu, sta, co, si}) ||
+      rows_overlap(to, rows_of(v, vts, vhs, tokens, H, D, dtype)) || any_overlap(ro, {tab, cu, sta, co, si, qn, kn}) ||
       any_overlap(ro, {ck, cv, ks, vs, bad}) || any_overlap(bad, {ck, cv, ks, vs}) || any_overlap(ks, {ck, cv, vs}) ||
       any_overlap(vs, {ck, cv}) || any_overlap(ck, {cv}))
     return LOWBIT_ERR_OVERLAP;
@@ -746,66 +771,42 @@ int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_tabl
   g.sin = sin;
   g.rope_rows = rope_rows;
   g.bad = bad_count;
+  g.q_norm = norms.q;
+  g.k_norm = norms.k;
+  g.norm_dtype = norms.dtype;
+  g.eps = norms.eps;
   return lowbit::launch_kv_append(g, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
 }
 
-int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
-                       const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
-                       int64_t max_tokens, int32_t dtype, void* k, int64_t kts, int64_t khs, void* v, int64_t vts,
-                       int64_t vhs, void* stream) {
-  if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16 && dtype != LOWBIT_F32) return LOWBIT_ERR_DTYPE;
-  int32_t st = check_cache(cache, block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
-  if (st) return st;
-  if (!tokens) return LOWBIT_OK;
-  const int64_t H = cache->kv_heads, D = cache->head_dim;
-  if ((st = check_rows(k, kts, khs, tokens, H, D, true))) return st;
-  if ((st = check_rows(v, vts, vhs, tokens, H, D, true))) return st;
-  const int64_t cb = cache_bytes(cache), sb = cache->pages * H * 4;
-  const Range rk = rows_range(k, kts, khs, tokens, H, D, dtype), rv = rows_range(v, vts, vhs, tokens, H, D, dtype);
-  for (const Range& w : {rk, rv})
-    if (any_overlap(w, {{cache->k, cb}, {cache->v, cb}, {cache->k_scale, sb}, {cache->v_scale, sb},
-                        {block_table, batch * table_width * 4}, {cu_tokens, (batch + 1) * 4}, {starts, batch * 4}}))
-      return LOWBIT_ERR_OVERLAP;
-  if (rows_overlap(rows_of(k, kts, khs, tokens, H, D, dtype), rows_of(v, vts, vhs, tokens, H, D, dtype)))
-    return LOWBIT_ERR_OVERLAP;
-  st = current_device(nullptr);
-  if (st) return st;
-  lowbit::KvReadArgs g{};
-  g.c = cache_args(cache);
-  g.t = table_args(block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
-  g.k = {k, kts, khs};
-  g.v = {v, vts, vhs};
-  g.dtype = dtype;
-  return lowbit::launch_kv_read(g, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
-}
-
-static size_t attention_bytes(int splits, int64_t tokens, int64_t q_heads, int64_t D) {
+size_t attention_bytes(int splits, int64_t tokens, int64_t q_heads, int64_t D) {
   return splits > 1 ? (size_t)splits * tokens * q_heads * (D + 2) * sizeof(float) : 0;
 }
 
-size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
-                                        int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window) {
+size_t attention_workspace(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len, int64_t q_heads,
+                           int64_t kv_heads, int64_t head_dim, int64_t window, int64_t sinks) {
   if (batch < 1 || tokens < 1 || max_tokens < 1 || max_len < 0 || kv_heads < 1 || q_heads < kv_heads || window < 0 ||
-      batch > 65535 || tokens >= kMaxDim || q_heads > 65536 || max_len > ((int64_t)1 << 30))
+      sinks < 0 ||      batch > 65535 || tokens >= kMaxDim || q_heads > 65536 || max_len > ((int64_t)1 << 30))
     return 0;
   int num_cu = 0;
   if (current_device(&num_cu) != LOWBIT_OK) num_cu = 256;   // no gfx950 device: the MI355X's count
   const lowbit::AttnPlan p =
       lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
-                             (int)std::min(window, max_len), (int)head_dim, num_cu);
+                             (int)std::min(window, max_len), window ? (int)std::min(sinks, max_len) : 0, (int)head_dim,
+                             num_cu);
   return attention_bytes(p.splits, tokens, q_heads, head_dim);
 }
 
-int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
-                         const int32_t* cu_tokens, const int32_t* lens, int64_t batch, int64_t tokens,
-                         int64_t max_tokens, int64_t max_len, int32_t dtype, const void* q, int64_t qts, int64_t qhs,
-                         int64_t q_heads, void* out, int64_t ots, int64_t ohs, float* lse, float scale,
-                         int32_t causal, int64_t window, void* workspace, size_t workspace_bytes, void* stream) {
+int32_t attention(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                  const int32_t* cu_tokens, const int32_t* lens, int64_t batch, int64_t tokens, int64_t max_tokens,
+                  int64_t max_len, int32_t dtype, const void* q, int64_t qts, int64_t qhs, int64_t q_heads, void* out,
+                  int64_t ots, int64_t ohs, float* lse, float scale, int32_t causal, int64_t window, int64_t sinks,
+                  void* workspace, size_t workspace_bytes, void* stream) {
   if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16) return LOWBIT_ERR_DTYPE;
   int32_t st = check_cache(cache, block_table, table_width, cu_tokens, lens, batch, tokens, max_tokens);
   if (st) return st;
   const int64_t H = cache->kv_heads, D = cache->head_dim;
-  if (q_heads < 1 || q_heads > 65536 || q_heads % H || max_len < 0 || max_len > ((int64_t)1 << 30) || window < 0)
+  if (q_heads < 1 || q_heads > 65536 || q_heads % H || max_len < 0 || max_len > ((int64_t)1 << 30) || window < 0 ||
+      sinks < 0)
     return LOWBIT_ERR_SHAPE;
   if (!tokens) return LOWBIT_OK;
   max_tokens = std::min(max_tokens, tokens);
@@ -841,9 +842,10 @@ int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_tabl
   a.causal = causal != 0;
   // a window that holds every token is none for the plan; the mask takes it as it is
   a.window = (int)std::min<int64_t>(window, (int64_t)1 << 30);
+  a.sinks = window ? (int)std::min(sinks, max_len) : 0;
   a.max_len = (int)max_len;
   const lowbit::AttnPlan p = lowbit::attention_plan(batch, (int)H, a.group, max_tokens, max_len,
-                                                    (int)std::min(window, max_len), (int)D, num_cu);
+                                                    (int)std::min(window, max_len), a.sinks, (int)D, num_cu);
   a.splits = p.splits;
   a.split_len = p.split_len;
   const size_t need = attention_bytes(a.splits, tokens, q_heads, D);
@@ -851,6 +853,299 @@ int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_tabl
   if (need && !aligned(workspace, 256)) return LOWBIT_ERR_ALIGN;
   a.part = (float*)workspace;
   return lowbit::launch_attention(a, p, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+}  // namespace
+
+extern "C" {
+
+int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                         const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                         int64_t max_tokens, int32_t dtype, const void* k, int64_t kts, int64_t khs, const void* v,
+                         int64_t vts, int64_t vhs, const void* q, int64_t qts, int64_t qhs, int64_t q_heads,
+                         void* q_out, int64_t ots, int64_t ohs, const float* cos, const float* sin, int64_t rot,
+                         int64_t rope_rows, int32_t interleaved, int32_t* bad_count, void* stream) {
+  return kv_append(cache, block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens, dtype, k, kts, khs, v,
+                   vts, vhs, q, qts, qhs, q_heads, q_out, ots, ohs, cos, sin, rot, rope_rows, interleaved,
+                   {nullptr, nullptr, LOWBIT_NONE, 0.0f}, bad_count, stream);
+}
+
+int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                       const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                       int64_t max_tokens, int32_t dtype, void* k, int64_t kts, int64_t khs, void* v, int64_t vts,
+                       int64_t vhs, void* stream) {
+  if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16 && dtype != LOWBIT_F32) return LOWBIT_ERR_DTYPE;
+  int32_t st = check_cache(cache, block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
+  if (st) return st;
+  if (!tokens) return LOWBIT_OK;
+  const int64_t H = cache->kv_heads, D = cache->head_dim;
+  if ((st = check_rows(k, kts, khs, tokens, H, D, true))) return st;
+  if ((st = check_rows(v, vts, vhs, tokens, H, D, true))) return st;
+  const int64_t cb = cache_bytes(cache), sb = cache->pages * H * 4;
+  const Range rk = rows_range(k, kts, khs, tokens, H, D, dtype), rv = rows_range(v, vts, vhs, tokens, H, D, dtype);
+  for (const Range& w : {rk, rv})
+    if (any_overlap(w, {{cache->k, cb}, {cache->v, cb}, {cache->k_scale, sb}, {cache->v_scale, sb},
+                        {block_table, batch * table_width * 4}, {cu_tokens, (batch + 1) * 4}, {starts, batch * 4}}))
+      return LOWBIT_ERR_OVERLAP;
+  if (rows_overlap(rows_of(k, kts, khs, tokens, H, D, dtype), rows_of(v, vts, vhs, tokens, H, D, dtype)))
+    return LOWBIT_ERR_OVERLAP;
+  st = current_device(nullptr);
+  if (st) return st;
+  lowbit::KvReadArgs g{};
+  g.c = cache_args(cache);
+  g.t = table_args(block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens);
+  g.k = {k, kts, khs};
+  g.v = {v, vts, vhs};
+  g.dtype = dtype;
+  return lowbit::launch_kv_read(g, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
+                                        int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window) {
+  return attention_workspace(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, window, 0);
+}
+
+int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                         const int32_t* cu_tokens, const int32_t* lens, int64_t batch, int64_t tokens,
+                         int64_t max_tokens, int64_t max_len, int32_t dtype, const void* q, int64_t qts, int64_t qhs,
+                         int64_t q_heads, void* out, int64_t ots, int64_t ohs, float* lse, float scale,
+                         int32_t causal, int64_t window, void* workspace, size_t workspace_bytes, void* stream) {
+  return attention(cache, block_table, table_width, cu_tokens, lens, batch, tokens, max_tokens, max_len, dtype, q, qts,
+                   qhs, q_heads, out, ots, ohs, lse, scale, causal, window, 0, workspace, workspace_bytes, stream);
+}
+
+int32_t lowbit_kv_append_norm(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                              const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                              int64_t max_tokens, int32_t dtype, const void* k, int64_t kts, int64_t khs,
+                              const void* v, int64_t vts, int64_t vhs, const void* q, int64_t qts, int64_t qhs,
+                              int64_t q_heads, void* q_out, int64_t ots, int64_t ohs, const float* cos,
+                              const float* sin, int64_t rot, int64_t rope_rows, int32_t interleaved,
+                              const void* q_norm, const void* k_norm, int32_t norm_dtype, float eps,
+                              int32_t* bad_count, void* stream) {
+  return kv_append(cache, block_table, table_width, cu_tokens, starts, batch, tokens, max_tokens, dtype, k, kts, khs, v,
+                   vts, vhs, q, qts, qhs, q_heads, q_out, ots, ohs, cos, sin, rot, rope_rows, interleaved,
+                   {q_norm, k_norm, norm_dtype, eps}, bad_count, stream);
+}
+
+int32_t lowbit_attention_sinks(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                               const int32_t* cu_tokens, const int32_t* lens, int64_t batch, int64_t tokens,
+                               int64_t max_tokens, int64_t max_len, int32_t dtype, const void* q, int64_t qts,
+                               int64_t qhs, int64_t q_heads, void* out, int64_t ots, int64_t ohs, float* lse,
+                               float scale, int32_t causal, int64_t window, int64_t sinks, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+  return attention(cache, block_table, table_width, cu_tokens, lens, batch, tokens, max_tokens, max_len, dtype, q, qts,
+                   qhs, q_heads, out, ots, ohs, lse, scale, causal, window, sinks, workspace, workspace_bytes, stream);
+}
+
+size_t lowbit_attention_sinks_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
+                                              int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window,
+                                              int64_t sinks) {
+  return attention_workspace(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, window, sinks);
+}
+
+int32_t lowbit_norm_rotate(int32_t dtype, int64_t tokens, int64_t head_dim, const void* q, int64_t qts, int64_t qhs,
+                           int64_t q_heads, void* q_out, int64_t ots, int64_t ohs, const void* k, int64_t kts,
+                           int64_t khs, int64_t k_heads, void* k_out, int64_t kots, int64_t kohs, const void* q_norm,
+                           const void* k_norm, int32_t norm_dtype, float eps, const float* cos, const float* sin,
+                           int64_t rot, int64_t rope_rows, const int32_t* positions, int32_t interleaved,
+                           int32_t* bad_count, void* stream) {
+  if (dtype != LOWBIT_F16 && dtype != LOWBIT_BF16 && dtype != LOWBIT_F32) return LOWBIT_ERR_DTYPE;
+  if (!head_size(head_dim) || tokens < 0 || tokens >= kMaxDim || q_heads < 1 || q_heads > 65536) return LOWBIT_ERR_SHAPE;
+  const bool keys = k != nullptr;
+  if (keys != (k_out != nullptr)) return LOWBIT_ERR_NULL;
+  if (keys && (k_heads < 1 || k_heads > 65536)) return LOWBIT_ERR_SHAPE;
+  if (rot < 0 || rot > head_dim || rot % 32 || (rot && (rope_rows < 1 || rope_rows >= kMaxDim))) return LOWBIT_ERR_SHAPE;
+  if ((rot != 0) != (cos != nullptr) || (rot != 0) != (sin != nullptr) || (positions && !rot)) return LOWBIT_ERR_NULL;
+  if (!rot && !q_norm && !k_norm) return LOWBIT_ERR_NULL;   // neither a norm nor a rotation
+  const Norms norms{q_norm, k_norm, norm_dtype, eps};
+  if (k_norm && !keys && tokens) return LOWBIT_ERR_NULL;
+  int32_t st = check_norms(norms, true);
+  if (st) return st;
+  if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(positions, 4) || !aligned(bad_count, 4)) return LOWBIT_ERR_ALIGN;
+  if (!tokens) return LOWBIT_OK;
+  if ((st = check_rows(q, qts, qhs, tokens, q_heads, head_dim, false))) return st;
+  if ((st = check_rows(q_out, ots, ohs, tokens, q_heads, head_dim, true))) return st;
+  if (keys && (st = check_rows(k, kts, khs, tokens, k_heads, head_dim, false))) return st;
+  if (keys && (st = check_rows(k_out, kots, kohs, tokens, k_heads, head_dim, true))) return st;
+  const Range co{cos, rope_rows * rot * 2}, si{sin, rope_rows * rot * 2}, po{positions, tokens * 4},
+              qn{q_norm, norms.bytes(head_dim)}, kn{k_norm, norms.bytes(head_dim)}, bad{bad_count, 4},
+              rq = rows_range(q, qts, qhs, tokens, q_heads, head_dim, dtype),
+              rk = rows_range(k, kts, khs, tokens, keys ? k_heads : 1, head_dim, dtype),
+              rqo = rows_range(q_out, ots, ohs, tokens, q_heads, head_dim, dtype),
+              rko = rows_range(k_out, kots, kohs, tokens, keys ? k_heads : 1, head_dim, dtype);
+  for (const Range& w : {rqo, rko, bad})
+    if (any_overlap(w, {co, si, po, qn, kn})) return LOWBIT_ERR_OVERLAP;
+  if (any_overlap(bad, {rq, rk, rqo, rko})) return LOWBIT_ERR_OVERLAP;
+  const Rows q_in = rows_of(q, qts, qhs, tokens, q_heads, head_dim, dtype),
+             q_to = rows_of(q_out, ots, ohs, tokens, q_heads, head_dim, dtype);
+  if (!(q == q_out && qts == ots && qhs == ohs) && rows_overlap(q_to, q_in)) return LOWBIT_ERR_OVERLAP;
+  if (keys) {
+    const Rows k_in = rows_of(k, kts, khs, tokens, k_heads, head_dim, dtype),
+               k_to = rows_of(k_out, kots, kohs, tokens, k_heads, head_dim, dtype);
+    if ((!(k == k_out && kts == kots && khs == kohs) && rows_overlap(k_to, k_in)) || rows_overlap(q_to, k_in) ||
+        rows_overlap(k_to, q_in) || rows_overlap(q_to, k_to))
+      return LOWBIT_ERR_OVERLAP;
+  }
+  if ((st = current_device(nullptr))) return st;
+  lowbit::TurnArgs g{};
+  g.in[0] = {(void*)q, qts, qhs};
+  g.in[1] = {(void*)k, kts, khs};
+  g.out[0] = {q_out, ots, ohs};
+  g.out[1] = {k_out, kots, kohs};
+  g.heads[0] = (int)q_heads;
+  g.heads[1] = keys ? (int)k_heads : 0;
+  g.w[0] = q_norm;
+  g.w[1] = k_norm;
+  g.D = (int)head_dim;
+  g.dtype = dtype;
+  g.w_dtype = norm_dtype;
+  g.rot = (int)rot;
+  g.inter = interleaved != 0;
+  g.eps = eps;
+  g.cos = cos;
+  g.sin = sin;
+  g.rope_rows = rope_rows;
+  g.pos = positions;
+  g.tokens = tokens;
+  g.bad = bad_count;
+  return lowbit::launch_norm_rotate(g, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+int32_t lowbit_rope_tables(float* cos, float* sin, int64_t positions, int64_t rot, int64_t first, double base,
+                           int32_t scaling, double factor, double original, double low, double high, double magnitude,
+                           void* stream) {
+  if (scaling < LOWBIT_ROPE_PLAIN || scaling > LOWBIT_ROPE_WAVELENGTH) return LOWBIT_ERR_DTYPE;
+  const double most = 1e300;                                // written so that NaN fails
+  if (positions < 0 || first < 0 || positions > kMaxDim || first > kMaxDim || first + positions > kMaxDim || rot < 32 ||
+      rot > 2 * lowbit::kMaxPairs || rot % 32 || !(base > 1.0 && base <= most) || !(magnitude >= 0.0 && magnitude <= 1e30))
+    return LOWBIT_ERR_SHAPE;
+  const bool bands = scaling == LOWBIT_ROPE_YARN || scaling == LOWBIT_ROPE_WAVELENGTH;
+  if (scaling != LOWBIT_ROPE_PLAIN && !(factor >= 1.0 && factor <= most)) return LOWBIT_ERR_SHAPE;
+  if (bands && (!(original > 0.0 && original <= most) || !(low > 0.0) || !(high > low && high <= most))) return LOWBIT_ERR_SHAPE;
+  if (positions && (!cos || !sin)) return LOWBIT_ERR_NULL;
+  if (!aligned(cos, 16) || !aligned(sin, 16)) return LOWBIT_ERR_ALIGN;
+  if (!positions) return LOWBIT_OK;
+  if (overlaps(cos, positions * rot * 2, sin, positions * rot * 2)) return LOWBIT_ERR_OVERLAP;
+  int32_t st = current_device(nullptr);
+  if (st) return st;
+  lowbit::TableArgs g{};
+  g.cos = cos;
+  g.sin = sin;
+  g.n = positions;
+  g.first = first;
+  g.half = (int)rot / 2;
+  const double turn = 6.283185307179586476925287;
+  if (scaling == LOWBIT_ROPE_NTK) base *= std::pow(factor, (double)rot / (rot - 2));
+  // the dimension whose frequency makes `turns` turns over the original length
+  auto dimension = [&](double turns) { return rot * std::log(original / (turn * turns)) / (2 * std::log(base)); };
+  const double from = bands ? std::max(std::floor(dimension(high)), 0.0) : 0.0;
+  const double to = bands ? std::min(std::ceil(dimension(low)), (double)rot - 1) : 0.0;
+  for (int i = 0; i < g.half; ++i) {
+    double f = std::pow(base, -2.0 * i / rot);
+    double less = 0.0;                                       // share of the frequency that is divided by the factor
+    if (scaling == LOWBIT_ROPE_LINEAR) less = 1.0;
+    if (scaling == LOWBIT_ROPE_YARN) less = std::min(std::max((i - from) / std::max(to - from, 1e-3), 0.0), 1.0);
+    if (scaling == LOWBIT_ROPE_WAVELENGTH)
+      less = 1.0 - std::min(std::max((original * f / turn - low) / (high - low), 0.0), 1.0);
+    if (less > 0.0) f = f * (1.0 - less) + f / factor * less;
+    g.quarters[i] = f / turn * 4.0;
+  }
+  g.magnitude = magnitude > 0.0                 ? (float)magnitude
+                : scaling == LOWBIT_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0)
+                                              : 1.0f;
+  return lowbit::launch_rope_tables(g, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
+}
+
+int32_t lowbit_kv_copy_pages(const lowbit_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t pairs,
+                             const int32_t* count, void* stream) {
+  int32_t st = check_cache(cache, nullptr, 0, nullptr, nullptr, 0, 0, 0);
+  if (st) return st;
+  if (pairs < 0 || pairs >= kMaxDim) return LOWBIT_ERR_SHAPE;
+  if (!aligned(src, 4) || !aligned(dst, 4) || !aligned(count, 4)) return LOWBIT_ERR_ALIGN;
+  if (!pairs) return LOWBIT_OK;
+  if (!src || !dst) return LOWBIT_ERR_NULL;
+  const int64_t cb = cache_bytes(cache), sb = cache->pages * cache->kv_heads * 4;
+  const Range ck{cache->k, cb}, cv{cache->v, cb}, ks{cache->k_scale, sb}, vs{cache->v_scale, sb};
+  for (const Range& w : {ck, cv, ks, vs})
+    if (any_overlap(w, {{src, pairs * 4}, {dst, pairs * 4}, {count, 4}})) return LOWBIT_ERR_OVERLAP;
+  if (any_overlap(ks, {ck, cv, vs}) || any_overlap(vs, {ck, cv}) || any_overlap(ck, {cv})) return LOWBIT_ERR_OVERLAP;
+  int num_cu = 0;
+  if ((st = current_device(&num_cu))) return st;
+  return lowbit::launch_copy_pages(cache_args(cache), src, dst, (int)pairs, count, num_cu, (hipStream_t)stream) == hipSuccess
+             ? LOWBIT_OK
+             : LOWBIT_ERR_HIP;
+}
+
+static bool remap_shape(int64_t batch, int64_t width, int64_t new_batch, int64_t new_width, int64_t pages) {
+  return batch >= 0 && batch <= 65535 && new_batch >= 0 && new_batch <= 65535 && width >= 0 && new_width >= 0 &&
+         width < kMaxDim && new_width < kMaxDim && new_batch * std::max(width, new_width) < kMaxDim && pages >= 1 &&
+         pages < kMaxDim;
+}
+
+int64_t lowbit_kv_remap_pairs(int64_t table_width, int64_t new_batch, int64_t pages, int32_t compact) {
+  if (!remap_shape(0, table_width, new_batch, 0, pages)) return -1;
+  return new_batch + (compact ? std::min(pages / 2, new_batch * table_width) : 0);
+}
+
+size_t lowbit_kv_remap_workspace_bytes(int64_t new_batch, int64_t pages) {
+  if (!remap_shape(0, 0, new_batch, 0, pages)) return 0;
+  return lowbit::remap_workspace(new_batch, pages);
+}
+
+int32_t lowbit_kv_remap(const int32_t* block_table, int64_t table_width, const int32_t* lens, int64_t batch,
+                        int64_t pages, int32_t page, const int32_t* rows, const int32_t* room, int64_t new_batch,
+                        int64_t window, int64_t sinks, int32_t compact, int32_t* new_table, int64_t new_width,
+                        int32_t* new_lens, int32_t* src, int32_t* dst, int64_t pairs, int32_t* counts,
+                        void* workspace, size_t workspace_bytes, void* stream) {
+  if (!page_size(page) || !remap_shape(batch, table_width, new_batch, new_width, pages) || window < 0 || sinks < 0 ||
+      pairs < lowbit_kv_remap_pairs(table_width, new_batch, pages, compact) || pairs >= kMaxDim ||
+      (!rows && new_batch && new_batch != batch))           // an empty array may have no address
+    return LOWBIT_ERR_SHAPE;
+  if ((batch && (!lens || (!block_table && table_width))) || (new_batch && (!new_lens || (!new_table && new_width))) ||
+      (pairs && (!src || !dst)) || !counts)
+    return LOWBIT_ERR_NULL;
+  for (const void* p : {(const void*)block_table, (const void*)lens, (const void*)rows, (const void*)room,
+                        (const void*)new_table, (const void*)new_lens, (const void*)src, (const void*)dst,
+                        (const void*)counts})
+    if (!aligned(p, 4)) return LOWBIT_ERR_ALIGN;
+  const size_t need = lowbit::remap_workspace(new_batch, pages);
+  if (!workspace || workspace_bytes < need) return LOWBIT_ERR_WORKSPACE;
+  if (!aligned(workspace, 256)) return LOWBIT_ERR_ALIGN;
+  const Range out[] = {{new_table, new_batch * new_width * 4}, {new_lens, new_batch * 4}, {src, pairs * 4},
+                       {dst, pairs * 4}, {counts, 16}, {workspace, (int64_t)need}};
+  for (const Range& w : out) {
+    if (any_overlap(w, {{block_table, batch * table_width * 4}, {lens, batch * 4}, {rows, new_batch * 4},
+                        {room, new_batch * 4}}))
+      return LOWBIT_ERR_OVERLAP;
+    for (const Range& x : out)
+      if (&x != &w && any_overlap(w, {x})) return LOWBIT_ERR_OVERLAP;
+  }
+  int num_cu = 0;
+  int32_t st = current_device(&num_cu);
+  if (st) return st;
+  lowbit::RemapArgs g{};
+  g.table = block_table;
+  g.lens = lens;
+  g.rows = rows;
+  g.room = room;
+  g.width = table_width;
+  g.width_out = new_width;
+  g.pages = pages;
+  g.batch = (int)batch;
+  g.new_batch = (int)new_batch;
+  g.page = page;
+  g.shift = __builtin_ctz(page);
+  g.compact = compact != 0;
+  g.most = (int)std::min<int64_t>(std::min(table_width, new_width) * page, 0x7fffffff);
+  g.window = std::min<int64_t>(window, kMaxDim);            // larger ones hold every token
+  g.sinks = sinks;
+  g.table_out = new_table;
+  g.lens_out = new_lens;
+  g.src = src;
+  g.dst = dst;
+  g.capacity = pairs;
+  g.counts = counts;
+  return lowbit::launch_remap(g, workspace, num_cu, (hipStream_t)stream) == hipSuccess ? LOWBIT_OK : LOWBIT_ERR_HIP;
 }
 
 int32_t lowbit_gelu(const void* in, void* out, int32_t dtype, int64_t count, void* stream) {

@@ -32,6 +32,10 @@
 //    maximum.
 //  * A page whose table entry is no page, and a token that the mask hides,
 //    have t = -inf. A row that keeps nothing gives zeros (and lse = -inf).
+//  * With a window and first tokens that stay visible, a row tile's context is
+//    two runs of tokens: the first ones, rounded up to 16, and from the first
+//    row's window on. The kernels walk them as one run of 16-token tiles, so
+//    that parts, segments and steps are those of a context without the gap.
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
@@ -94,12 +98,16 @@ __device__ __forceinline__ float sum16(float x) { return sum32(x + __shfl_xor(x,
 // What one row tile has to do: rows [row0, row0 + rows) of (token, head in
 // group) pairs of one sequence and key/value head, tokens [t0, t1) of its
 // context.
+// (SINKS: a place u of the tile's context is token u before `head`, token u + skip from there on; t0 and t1 are places,
+// t1 .. end the last one's token. Else places are tokens.)
 struct Work {
   int64_t lo;                              // first row of the sequence in the dense operands
-  int n, rows, row0, len, t0, t1;
+  int n, rows, row0, len, t0, t1, end, head, skip;
   __device__ __forceinline__ int pos(int row, int group) const { return len - n + row / group; }
+  template <bool SINKS> __device__ __forceinline__ int token(int u) const { return SINKS && u >= head ? u + skip : u; }
 };
 
+template <bool SINKS>
 __device__ __forceinline__ bool find_work(const AttnArgs& a, int b, int row0, int tile, int split, Work* w) {
   kv_rows(a.t, b, &w->lo, &w->n);
   w->rows = min(tile, w->n * a.group - row0);
@@ -109,11 +117,50 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int b, int row0, in
   int len = max(0, min(a.t.start[b], a.max_len));
   w->len = len = (int)min((int64_t)len, room);
   const int last = w->pos(row0 + w->rows - 1, a.group), first = w->pos(row0, a.group);
-  const int end = a.causal ? max(0, min(len, last + 1)) : len;
-  const int beg = a.window ? max(0, first - a.window + 1) & ~15 : 0;
+  int end = a.causal ? max(0, min(len, last + 1)) : len;
+  int beg = a.window ? max(0, first - a.window + 1) & ~15 : 0;
+  w->head = w->skip = 0;
+  if (SINKS) {
+    const int head = (a.sinks + 15) & ~15;
+    if (beg > head) {
+      w->head = head;
+      w->skip = beg - head;
+      end = max(0, end - w->skip);
+    }
+    beg = 0;
+  }
   w->t0 = (int)min((int64_t)end, beg + (int64_t)split * a.split_len);
   w->t1 = (int)min((int64_t)end, beg + ((int64_t)split + 1) * a.split_len);
+  w->end = SINKS && w->t1 > w->head ? w->t1 + w->skip : w->t1;
   return true;
+}
+
+// The pages of the places [from, to) of a tile's context, as they stand in LDS:
+// `two` of them (SINKS) are those before the gap.
+struct Run {
+  int first, second, two, n;               // first page of the run, of its part behind the gap
+  // where the page of token t at place u stands
+  template <bool SINKS> __device__ __forceinline__ int at(const Work& w, int u, int t, int shift) const {
+    return (t >> shift) - (SINKS && u >= w.head ? second - two : first);
+  }
+  template <bool SINKS> __device__ __forceinline__ int page(int i) const {
+    return SINKS && i >= two ? second + i - two : first + i;
+  }
+};
+template <bool SINKS>
+__device__ __forceinline__ Run find_run(const Work& w, int from, int to, int shift) {
+  Run r;
+  const int last = (w.token<SINKS>(to - 1)) >> shift;
+  r.first = from >> shift;
+  r.second = r.two = 0;
+  if (SINKS) {
+    r.second = w.token<SINKS>(max(from, w.head)) >> shift;
+    if (from < w.head) r.two = ((min(to, w.head) - 1) >> shift) - r.first + 1;
+    r.n = r.two + (to > w.head ? last - r.second + 1 : 0);
+  } else {
+    r.n = last - r.first + 1;
+  }
+  return r;
 }
 
 // Row (token row, head) of the dense operands for row r of the tile.
@@ -123,11 +170,12 @@ __device__ __forceinline__ void row_place(const AttnArgs& a, const Work& w, int 
   *head = h * a.group + row % a.group;
 }
 
-// The pages p0 .. p0 + np - 1 of sequence b: their blocks into LDS, then (by
-// the same threads) the blocks' scales.
-__device__ __forceinline__ void find_pages(const AttnArgs& a, int b, int h, int p0, int np, Pages* pg) {
-  for (int i = threadIdx.x; i < np; i += blockDim.x) {
-    const int32_t id = a.t.table[(int64_t)b * a.t.width + p0 + i];
+// The pages of a run of sequence b: their blocks into LDS, then (by the same
+// threads) the blocks' scales.
+template <bool SINKS>
+__device__ __forceinline__ void find_pages(const AttnArgs& a, int b, int h, const Run& run, Pages* pg) {
+  for (int i = threadIdx.x; i < run.n; i += blockDim.x) {
+    const int32_t id = a.t.table[(int64_t)b * a.t.width + run.page<SINKS>(i)];
     const bool there = id >= 0 && id < a.c.pages;
     pg->blk[i] = there ? id * a.c.heads + h : 0;
     pg->lv[i] = there ? 0.0f : NEG_INF;
@@ -188,7 +236,7 @@ __device__ __forceinline__ void store_lse(const AttnArgs& a, int64_t token, int 
 // ONCE: one row tile a sequence and head, so the cache is read once, past the
 // L2 (two sequences of 131072 tokens: 79 us against 90; with three row tiles
 // 25 against 23).
-template <bool BF16, int D, bool ONCE>
+template <bool BF16, int D, bool ONCE, bool SINKS>
 __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
   constexpr int NW = 4, NI = D / 64, LD = D + 4, STEP = 32 * NW;
   constexpr float TOP = 14.0f, UNSHIFT = 0x1p-14f;                     // p' up to 2^14
@@ -200,9 +248,8 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
   const int g = lane >> 4, r = lane & 15;
   const int split = blockIdx.x, h = blockIdx.y % a.c.heads, b = blockIdx.z;
   Work w;
-  if (!find_work(a, b, 16 * (blockIdx.y / a.c.heads), 16, split, &w)) return;
+  if (!find_work<SINKS>(a, b, 16 * (blockIdx.y / a.c.heads), 16, split, &w)) return;
   const int shift = 31 - __builtin_clz(a.c.page);
-  const int p0 = w.t0 >> shift;
 
   float m = NEG_INF, l = 0.0f;
   f32x4 o[D / 16];
@@ -223,9 +270,14 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) vr[j][i] = load(a.c.v + at + g * 4 * D + r * 16 + 256 * i);
     };
-    // the 16-token tile at t (clamped into the part) of block blk
+    // the 16-token tile at place t (clamped into the part) of block blk
     auto tile_at = [&](int t, int32_t blk) __attribute__((always_inline)) {
-      return ((int64_t)blk << shift) * D + (int64_t)(min(t, last) & (a.c.page - 1)) * D;
+      return ((int64_t)blk << shift) * D + (int64_t)(w.token<SINKS>(min(t, last)) & (a.c.page - 1)) * D;
+    };
+    const Run run = find_run<SINKS>(w, w.t0, w.t1, shift);
+    auto page_at = [&](int t) __attribute__((always_inline)) {         // where its page stands in LDS
+      t = min(t, last);
+      return run.at<SINKS>(w, t, w.token<SINKS>(t), shift);
     };
     // the first step's tiles straight from the table: their loads and those of the scales are under way together
     int t = (w.t0 & ~15) + 32 * wave;
@@ -233,7 +285,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       int64_t at[2];
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int32_t id = a.t.table[(int64_t)b * a.t.width + (min(t + 16 * j, last) >> shift)];
+        const int32_t id = a.t.table[(int64_t)b * a.t.width + (w.token<SINKS>(min(t + 16 * j, last)) >> shift)];
         at[j] = tile_at(t + 16 * j, id >= 0 && id < a.c.pages ? id * a.c.heads + h : 0);
       }
 #pragma unroll
@@ -241,8 +293,8 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) load_v(j, at[j]);
     }
-    find_pages(a, b, h, p0, ((w.t1 - 1) >> shift) - p0 + 1, &pg);
-    load_scales(a, ((w.t1 - 1) >> shift) - p0 + 1, 1.0f, &pg);
+    find_pages<SINKS>(a, b, h, run, &pg);
+    load_scales(a, run.n, 1.0f, &pg);
     // queries: lane (g, r) holds d = 16 (g + 4 i) + 8 half .. + 7 of row r
     int64_t token;
     int head;
@@ -270,10 +322,21 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
           for (int e = 0; e < 4; ++e) qf[i][k][e] = pack2(x[i][k][2 * e] * by, x[i][k][2 * e + 1] * by);
     }
     const int pos = w.pos(w.row0 + min(r, w.rows - 1), a.group);
-    const int hi = a.causal ? min(w.t1, pos + 1) : w.t1, lo = a.window ? pos - a.window + 1 : 0;
+    const int hi = a.causal ? min(w.end, pos + 1) : w.end, lo = a.window ? pos - a.window + 1 : 0;
     // tokens that no row of the tile masks
     const int pos0 = w.pos(w.row0, a.group), pos1 = w.pos(w.row0 + w.rows - 1, a.group);
-    const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = a.window ? pos1 - a.window + 1 : 0;
+    const int all_hi = a.causal ? min(w.end, pos0 + 1) : w.end, all_lo = a.window ? pos1 - a.window + 1 : 0;
+    // whether some row masks a token of the step at place t
+    auto masked = [&](int t) __attribute__((always_inline)) {
+      if constexpr (!SINKS) return t < all_lo || t < w.t0 || t + 32 > all_hi;
+      bool some = false;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int tok = w.token<SINKS>(t + 16 * j);
+        some |= tok + 16 > all_hi || (tok < all_lo && tok + 16 > a.sinks);
+      }
+      return some;
+    };
     __syncthreads();
 
     for (; t < w.t1; t += STEP) {
@@ -289,7 +352,7 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       }
       int64_t next[2];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) next[j] = tile_at(t + STEP + 16 * j, pg.blk[(min(t + STEP + 16 * j, last) >> shift) - p0]);
+      for (int j = 0; j < 2; ++j) next[j] = tile_at(t + STEP + 16 * j, pg.blk[page_at(t + STEP + 16 * j)]);
       if (t + STEP < w.t1) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) load_k(j, next[j]);
@@ -297,19 +360,19 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
       float rv[2], mx = NEG_INF;
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const int p = (min(t + 16 * j, last) >> shift) - p0;
+        const int p = page_at(t + 16 * j);
         const float kf = pg.kf[p] * qs, lv = pg.lv[p];
         rv[j] = pg.rv[p];
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = __builtin_fmaf(s[j][e], kf, lv);
       }
-      if (t < all_lo || t < w.t0 || t + 32 > all_hi) {
+      if (masked(t)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int tok = t + 16 * j + 4 * g + e;
-            if (tok < lo || tok < w.t0 || tok >= hi) s[j][e] = NEG_INF;
+            const int tok = w.token<SINKS>(t + 16 * j) + 4 * g + e;
+            if ((tok < lo && !(SINKS && tok < a.sinks)) || (!SINKS && tok < w.t0) || tok >= hi) s[j][e] = NEG_INF;
           }
       }
 #pragma unroll
@@ -422,7 +485,7 @@ __device__ __forceinline__ int many_run(const f32x16* o, int c, int hh, float* v
   return 128 * (c >> 2) + 4 * (8 * (c & 3) + 4 * hh);
 }
 
-template <bool BF16, int D, int W>
+template <bool BF16, int D, int W, bool SINKS>
 __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kernel(AttnArgs a) {
   constexpr int TOK = many::TOK, NT = 64 * W, ROWS = 32 * W;
   constexpr float SLACK = many::SLACK, TOP = many::TOP, UNSHIFT = many::UNSHIFT;
@@ -442,7 +505,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
   const int h = blockIdx.x % a.c.heads, split = blockIdx.x / a.c.heads, b = blockIdx.z;
   const int tile = b & 1 ? blockIdx.y : gridDim.y - 1 - blockIdx.y;
   Work w;
-  if (!find_work(a, b, ROWS * tile, ROWS, split, &w)) return;
+  if (!find_work<SINKS>(a, b, ROWS * tile, ROWS, split, &w)) return;
   const int shift = 31 - __builtin_clz(a.c.page);
 
   const int rr = min(32 * wave + r, w.rows - 1);
@@ -474,13 +537,36 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
     }
   };
   const int pos = w.pos(w.row0 + rr, a.group);
-  const int hi = a.causal ? min(w.t1, pos + 1) : w.t1, lo = max(w.t0, a.window ? pos - a.window + 1 : 0);
+  const int first = SINKS ? 0 : w.t0;                                  // no token before it is read
+  const int hi = a.causal ? min(w.end, pos + 1) : w.end, lo = max(first, a.window ? pos - a.window + 1 : 0);
   // tokens that no row of this wave masks
   const int f0 = min(32 * wave, w.rows - 1), f1 = min(32 * wave + 31, w.rows - 1);
   const int pos0 = w.pos(w.row0 + f0, a.group), pos1 = w.pos(w.row0 + f1, a.group);
-  const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = max(w.t0, a.window ? pos1 - a.window + 1 : 0);
+  const int all_hi = a.causal ? min(w.end, pos0 + 1) : w.end, all_lo = max(first, a.window ? pos1 - a.window + 1 : 0);
   // tokens that some row of this wave sees
-  const int any_hi = 32 * wave >= w.rows ? 0 : a.causal ? min(w.t1, pos1 + 1) : w.t1, any_lo = max(w.t0, a.window ? pos0 - a.window + 1 : 0);
+  const int any_hi = 32 * wave >= w.rows ? 0 : a.causal ? min(w.end, pos1 + 1) : w.end;
+  const int any_lo = max(first, a.window ? pos0 - a.window + 1 : 0);
+  // whether no row of this wave sees a token of the tile at place t, and whether some row masks one
+  auto unseen = [&](int t) __attribute__((always_inline)) {
+    if constexpr (!SINKS) return t >= any_hi || t + TOK <= any_lo;
+    bool all = true;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int tok = w.token<SINKS>(t + 16 * u);
+      all &= tok >= any_hi || (tok + 16 <= any_lo && tok >= a.sinks);
+    }
+    return all;
+  };
+  auto masked = [&](int t) __attribute__((always_inline)) {
+    if constexpr (!SINKS) return t < all_lo || t + TOK > all_hi;
+    bool some = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int tok = w.token<SINKS>(t + 16 * u);
+      some |= tok + 16 > all_hi || (tok < all_lo && tok + 16 > a.sinks);
+    }
+    return some;
+  };
 
   float m = NEG_INF, l = 0.0f;
   f32x16 o[D / 32];
@@ -493,14 +579,15 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
   const int tbeg = w.t0 & ~15;
   const int seg_tokens = (PAGES - 8) << shift;                         // tokens whose pages fit the LDS
   for (int seg = tbeg; seg < w.t1; seg += seg_tokens) {                // a multiple of 64 tokens
-    const int send = min(w.t1, seg + seg_tokens), p0 = seg >> shift, last = (send - 1) & ~15;
-    const int np = ((send - 1) >> shift) - p0 + 1;
+    const int send = min(w.t1, seg + seg_tokens), last = (send - 1) & ~15;
+    const Run run = find_run<SINKS>(w, seg, send, shift);
     if (seg != tbeg) __syncthreads();
-    find_pages(a, b, h, p0, np, &pg);
+    find_pages<SINKS>(a, b, h, run, &pg);
     __syncthreads();
-    auto tile_at = [&](int t) {                                        // bytes of the 16-token tile at t in its array
+    auto tile_at = [&](int t) {                                        // bytes of the 16-token tile at place t in its array
       t = min(t, last);
-      return ((int64_t)pg.blk[(t >> shift) - p0] << shift) * D + (int64_t)(t & (a.c.page - 1)) * D;
+      const int tok = w.token<SINKS>(t);
+      return ((int64_t)pg.blk[run.at<SINKS>(w, t, tok, shift)] << shift) * D + (int64_t)(tok & (a.c.page - 1)) * D;
     };
     auto words = [](uint32_t* to, const uint8_t* from, auto n) __attribute__((always_inline)) {
       constexpr int N = decltype(n)::value;
@@ -551,7 +638,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
     // Codes are fetched two tiles ahead and converted one tile ahead, between
     // the scores' matrix instructions; past the end the last tile repeats.
     fetch(seg);
-    load_scales(a, np, UNSHIFT, &pg);                                  // the sum takes the factor off again
+    load_scales(a, run.n, UNSHIFT, &pg);                                  // the sum takes the factor off again
     if (seg == tbeg) convert_queries();
     stage(smem);
     fetch(seg + TOK);
@@ -561,7 +648,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
       const uint8_t* ks = smem + buf * many::stage<D>();
       const uint8_t* vs = ks + KB;
       uint8_t* const to = smem + (buf ^ 1) * many::stage<D>();
-      if (t >= any_hi || t + TOK <= any_lo) {
+      if (unseen(t)) {
         stage(to);
         fetch(t + 2 * TOK);
       } else {
@@ -582,19 +669,19 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
         float rv[4], mx = NEG_INF;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int p = (min(t + 16 * u, last) >> shift) - p0;
+          const int at = min(t + 16 * u, last), p = run.at<SINKS>(w, at, w.token<SINKS>(at), shift);
           const float kf = pg.kf[p] * qs, lv = pg.lv[p] - low;
           rv[u] = pg.rv[p];
 #pragma unroll
           for (int e = 8 * (u & 1); e < 8 * (u & 1) + 8; ++e) s[u >> 1][e] = __builtin_fmaf(s[u >> 1][e], kf, lv);
         }
-        if (t < all_lo || t + TOK > all_hi) {
+        if (masked(t)) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int tok = t + 32 * j + (e & 3) + 8 * (e >> 2) + 4 * hh;
-              if (tok < lo || tok >= hi) s[j][e] = NEG_INF;
+              const int tok = w.token<SINKS>(t + 32 * j + 16 * (e >> 3)) + (e & 3) + 8 * (e >> 2 & 1) + 4 * hh;
+              if ((tok < lo && !(SINKS && tok < a.sinks)) || tok >= hi) s[j][e] = NEG_INF;
             }
         }
 #pragma unroll
@@ -737,23 +824,23 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a) {
 constexpr int FEW_ROWS = 80;
 constexpr int FEW_SPLIT = 4096;            // tokens of a part that PAGES covers at pages of 16 (plus one page of offset)
 
-template <bool BF16, int D, int W>
+template <bool BF16, int D, int W, bool SINKS>
 void launch_many(const AttnArgs& a, int rows, hipStream_t st) {
-  attend_many_kernel<BF16, D, W><<<dim3(a.c.heads * a.splits, (rows + 32 * W - 1) / (32 * W), a.t.batch), 64 * W,
+  attend_many_kernel<BF16, D, W, SINKS><<<dim3(a.c.heads * a.splits, (rows + 32 * W - 1) / (32 * W), a.t.batch), 64 * W,
                                    many::lds<D>(), st>>>(a);
 }
 
-template <bool BF16, int D>
+template <bool BF16, int D, bool SINKS>
 hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
   const int rows = a.t.max_tokens * a.group;
   if (p.few && rows <= 16)
-    attend_few_kernel<BF16, D, true><<<dim3(a.splits, a.c.heads, a.t.batch), 256, 0, st>>>(a);
+    attend_few_kernel<BF16, D, true, SINKS><<<dim3(a.splits, a.c.heads, a.t.batch), 256, 0, st>>>(a);
   else if (p.few)
-    attend_few_kernel<BF16, D, false><<<dim3(a.splits, a.c.heads * ((rows + 15) / 16), a.t.batch), 256, 0, st>>>(a);
+    attend_few_kernel<BF16, D, false, SINKS><<<dim3(a.splits, a.c.heads * ((rows + 15) / 16), a.t.batch), 256, 0, st>>>(a);
   else if (p.waves == 4)
-    launch_many<BF16, D, 4>(a, rows, st);
+    launch_many<BF16, D, 4, SINKS>(a, rows, st);
   else if constexpr (D == 128)
-    launch_many<BF16, D, 8>(a, rows, st);
+    launch_many<BF16, D, 8, SINKS>(a, rows, st);
   if (a.splits > 1) {
     const int64_t total = a.t.tokens * a.q_heads, nx = std::min<int64_t>(total, 1 << 22);   // nx * 256 threads fit 32 bits
     attend_join_kernel<BF16, D><<<dim3((unsigned)nx, (unsigned)((total + nx - 1) / nx)), 256, 0, st>>>(a);
@@ -775,13 +862,13 @@ hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
 // from Python; 8 of 2000: 13.2 in parts, 16.2 whole). But at least enough
 // parts of 1024 tokens to fill the GPU, since lengths are ragged.
 // Many rows: parts until the row tiles fill the GPU twice.
-AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int D,
-                        int num_cu) {
+AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
+                        int D, int num_cu) {
   const int64_t rows = max_tokens * group;
   AttnPlan p{};
   p.few = rows <= FEW_ROWS;
   int64_t span = max_len;
-  if (window) span = std::min(span, (int64_t)window + max_tokens + 16);
+  if (window) span = std::min(span, (int64_t)window + max_tokens + 16 + (sinks + 15) / 16 * 16);
   int64_t n = 1, len;
   if (p.few) {
     p.waves = 4;
@@ -821,11 +908,17 @@ AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens,
   return p;
 }
 
+template <bool BF16, bool SINKS>
+static hipError_t launch_heads(const AttnArgs& a, AttnPlan p, hipStream_t st) {
+  if (a.c.D == 64) return launch<BF16, 64, SINKS>(a, p, st);
+  if (a.c.D == 128) return launch<BF16, 128, SINKS>(a, p, st);
+  return launch<BF16, 256, SINKS>(a, p, st);
+}
+
 hipError_t launch_attention(const AttnArgs& a, AttnPlan p, hipStream_t st) {
   const bool bf = a.dtype == DT_BF16;
-  if (a.c.D == 64) return bf ? launch<true, 64>(a, p, st) : launch<false, 64>(a, p, st);
-  if (a.c.D == 128) return bf ? launch<true, 128>(a, p, st) : launch<false, 128>(a, p, st);
-  return bf ? launch<true, 256>(a, p, st) : launch<false, 256>(a, p, st);
+  if (a.sinks) return bf ? launch_heads<true, true>(a, p, st) : launch_heads<false, true>(a, p, st);
+  return bf ? launch_heads<true, false>(a, p, st) : launch_heads<false, false>(a, p, st);
 }
 
 }  // namespace lowbit

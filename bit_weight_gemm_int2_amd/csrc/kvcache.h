@@ -49,6 +49,10 @@ struct KvAppendArgs {
   const float* sin;
   int64_t rope_rows;
   int32_t* bad;           // nullable [2]: non-finite values, tokens without a place
+  const void* k_norm;     // nullable [D] of norm_dtype: weights of the heads' norms
+  const void* q_norm;
+  int norm_dtype;
+  float eps;
 };
 
 struct KvReadArgs {
@@ -75,6 +79,30 @@ __device__ __forceinline__ void kv_rows(const KvTable& t, int b, int64_t* lo, in
   *n = (int)(e - a < t.max_tokens ? e - a : t.max_tokens);
 }
 
+struct TurnArgs {         // norm and rotation of dense rows
+  KvRows in[2], out[2];   // queries, keys
+  int heads[2];           // 0: none
+  const void* w[2];       // nullable
+  int D, dtype, w_dtype, rot, inter;
+  float eps;
+  const float* cos;       // [rope_rows][rot / 2]
+  const float* sin;
+  int64_t rope_rows;
+  const int32_t* pos;     // nullable [tokens]: else token t is at position t
+  int64_t token0, tokens; // of this launch: token0 .. token0 + tokens - 1
+  int32_t* bad;           // nullable [1]: tokens without a position
+};
+
+constexpr int kMaxPairs = 128;      // rot / 2
+struct TableArgs {
+  float* cos;             // [n][half]
+  float* sin;
+  int64_t n, first;
+  int half;
+  float magnitude;
+  double quarters[kMaxPairs];       // a position's angle in quarter turns, at most 2 / pi
+};
+
 struct AttnArgs {
   KvCache c;
   KvTable t;              // start = tokens of each sequence in the cache, new ones included
@@ -84,6 +112,7 @@ struct AttnArgs {
   int dtype;
   float scale;            // times log2(e): the kernels work in powers of two
   int causal, window, max_len;
+  int sinks;              // first tokens seen beside the window, 0 without one
   int splits, split_len;  // parts of the context, one workgroup each
   float* part;            // splits > 1: [splits][tokens * q_heads][D], then (max, sum) [splits][tokens * q_heads]
 };

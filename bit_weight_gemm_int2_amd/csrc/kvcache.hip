@@ -1,8 +1,8 @@
 // Writing and reading the 8-bit paged key/value cache (layout: kvcache.h).
 //
 // Append: key rows are rotated by their position (pairs (x, y) of the first
-// `rot` dimensions become (x cos - y sin, x sin + y cos)), values are taken as
-// they are. A block's scale is s = max(s_old, a / 127) with a the largest
+// `rot` dimensions become (x cos - y sin, x sin + y cos)), after the norm of
+// the head where one is given; values are taken as they are. A block's scale is s = max(s_old, a / 127) with a the largest
 // magnitude among the block's new values (s_old = 0 for a block that starts
 // with this call), and a value r is stored as 128 + rint(r / s). When the
 // scale grows, the block's older codes c follow it as rint(c s_old / s): each
@@ -12,6 +12,7 @@
 // owns a block, so nothing is atomic and the result is a pure function of the
 // input.
 #include "kvcache.h"
+#include "rotate.h"
 
 namespace lowbit {
 
@@ -21,92 +22,6 @@ constexpr int MAX_THREADS = 1024;
 // scales below this are kept as 0 (reciprocals of scales stay finite); their values are
 // below 2^-93 and become 0
 constexpr float MIN_SCALE = 7.888609052210118e-31f;   // 2^-100
-
-// 8 consecutive values, 16-byte aligned. ONCE: values that nothing reads again
-// from the caches (non-temporal, as all dense stores: 11000 tokens with their
-// queries and the read-back took 86 us through the caches, 74 past them).
-template <int DT, bool ONCE = false>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float* r) {
-  if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const f32x4 w = *(const f32x4*)((const float*)p + i + 4 * j);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[4 * j + e] = w[e];
-    }
-  } else {
-    const u32x4* from = (const u32x4*)((const uint16_t*)p + i);
-    const u32x4 w = ONCE ? __builtin_nontemporal_load(from) : *from;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint16_t h = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
-      r[e] = DT == DT_F16 ? half_bits_to_float(h) : bf16_bits_to_float(h);
-    }
-  }
-}
-
-template <int DT>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float* r) {
-  if constexpr (DT == DT_F32) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-      __builtin_nontemporal_store(f32x4{r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]},
-                                  (f32x4*)((float*)p + i + 4 * j));
-  } else {
-    u32x4 w;
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      w[e] = DT == DT_F16 ? (uint32_t)float_to_half_bits(r[2 * e]) | (uint32_t)float_to_half_bits(r[2 * e + 1]) << 16
-                          : (uint32_t)float_to_bf16_bits(r[2 * e]) | (uint32_t)float_to_bf16_bits(r[2 * e + 1]) << 16;
-    __builtin_nontemporal_store(w, (u32x4*)((uint16_t*)p + i));
-  }
-}
-
-// Unit u of a row is 16 values in two pieces of 8, placed so that a rotated
-// pair never leaves a unit: with halves apart (d, d + rot / 2) the pieces are
-// 8 u and rot / 2 + 8 u, with neighbours paired (and past the rotated part)
-// they are 16 u and 16 u + 8. Every piece is one 16-byte load of 16-bit
-// values, and neighbouring lanes take neighbouring pieces.
-__device__ __forceinline__ void unit_places(int u, int rot, int inter, int* d0, int* d1) {
-  if (!inter && 16 * u < rot) {
-    *d0 = 8 * u;
-    *d1 = rot / 2 + 8 * u;
-  } else {
-    *d0 = 16 * u;
-    *d1 = 16 * u + 8;
-  }
-}
-
-struct Turn {             // cos and sin of a unit's eight pairs; none past the rotated part
-  float c[8], s[8];
-  bool on;
-};
-__device__ __forceinline__ void load_turn(const KvAppendArgs& g, int u, int64_t pos, Turn* t) {
-  t->on = 16 * u < g.rot;
-  if (!t->on) return;
-  load8<DT_F32>(g.cos, pos * (g.rot / 2) + 8 * u, t->c);
-  load8<DT_F32>(g.sin, pos * (g.rot / 2) + 8 * u, t->s);
-}
-
-// Rotate one unit in place: r[0 .. 7] is its first piece, r[8 .. 15] its second.
-__device__ __forceinline__ void rotate_unit(float* r, const Turn& t, int inter) {
-  if (!t.on) return;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int a = i, b = i + 8;
-    if (!inter) {
-      const float x = r[a], y = r[b];
-      r[a] = __builtin_fmaf(x, t.c[i], -(y * t.s[i]));
-      r[b] = __builtin_fmaf(x, t.s[i], y * t.c[i]);
-    } else {
-      const float x = r[2 * i], y = r[2 * i + 1];
-      r[2 * i] = __builtin_fmaf(x, t.c[i], -(y * t.s[i]));
-      r[2 * i + 1] = __builtin_fmaf(x, t.s[i], y * t.c[i]);
-    }
-  }
-}
-
-__device__ __forceinline__ bool finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 __device__ __forceinline__ uint32_t code(float r) {
   const float c = fminf(fmaxf(__builtin_rintf(r), -127.0f), 127.0f);
@@ -162,7 +77,7 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d, c
 // Both writers read their new values once: the first KEEP units of a thread
 // (all of them for blocks of 64 tokens of 128) stay in registers between the
 // maximum and the codes; larger blocks read the rest again.
-template <int DT>
+template <int DT, bool NORM>
 __device__ void append_keys(const KvAppendArgs& g, int64_t row0, int64_t pos0, int p0, int n, int64_t id, int h,
                             float* lds, int* bad) {
   constexpr int KEEP = 2;
@@ -171,6 +86,13 @@ __device__ void append_keys(const KvAppendArgs& g, int64_t row0, int64_t pos0, i
   float* sp = g.c.ks + id * g.c.heads + h;
   const float old = p0 ? *sp : 0.0f;
   const int shift = 31 - __builtin_clz(U);
+  const bool norm = NORM && g.k_norm != nullptr;
+  float wk[16];                                              // a thread's units are all at one place of their rows
+  if (norm) {
+    int d0, d1;
+    unit_places(threadIdx.x & (U - 1), g.rot, g.inter, &d0, &d1);
+    load_weights(g.k_norm, g.norm_dtype, d0, d1, wk);
+  }
   // unit i of the new rows, rotated; non-finite values are 0
   auto fetch = [&](int i, float* r) __attribute__((always_inline)) {
     const int t = i >> shift, u = i & (U - 1);
@@ -180,7 +102,8 @@ __device__ void append_keys(const KvAppendArgs& g, int64_t row0, int64_t pos0, i
     load8<DT>(g.k.p, at + d0, r);
     load8<DT>(g.k.p, at + d1, r + 8);
     Turn turn;
-    load_turn(g, u, pos0 + t, &turn);
+    load_turn(g.cos, g.sin, g.rot, u, pos0 + t, &turn);
+    if (norm) norm_unit(r, wk, U, 1.0 / D, g.eps);
     rotate_unit(r, turn, g.inter);
     int count = 0;
 #pragma unroll
@@ -337,7 +260,7 @@ __device__ void append_values(const KvAppendArgs& g, int64_t row0, int p0, int n
 // `rotated` of which have a position; the others' become 0. A thread takes one
 // unit of one token and walks the heads with its cos and sin in registers;
 // with few tokens the heads are spread over threads too.
-template <int DT>
+template <int DT, bool NORM>
 __device__ void rotate_queries(const KvAppendArgs& g, int64_t row0, int64_t pos0, int n, int rotated, int first,
                                int last) {
   const int U = g.c.D / 16, shift = 31 - __builtin_clz(U), units = rotated << shift;
@@ -351,17 +274,25 @@ __device__ void rotate_queries(const KvAppendArgs& g, int64_t row0, int64_t pos0
   }
   if (!units) return;
   const int ways = max(1, min(last - first, (int)blockDim.x / units));
+  const bool norm = NORM && g.q_norm != nullptr;
+  float wq[16];
+  if (norm) {
+    int d0, d1;
+    unit_places(threadIdx.x & (U - 1), g.rot, g.inter, &d0, &d1);
+    load_weights(g.q_norm, g.norm_dtype, d0, d1, wq);
+  }
   for (int i = threadIdx.x; i < units * ways; i += blockDim.x) {
     const int way = i / units, j = i - way * units, t = j >> shift, u = j & (U - 1);
     int d0, d1;
     unit_places(u, g.rot, g.inter, &d0, &d1);
     Turn turn;
-    load_turn(g, u, pos0 + t, &turn);
+    load_turn(g.cos, g.sin, g.rot, u, pos0 + t, &turn);
     const int64_t at = (row0 + t) * g.q.ts, to = (row0 + t) * g.qo.ts;
     for (int h = first + way; h < last; h += ways) {
       float r[16];
       load8<DT, true>(g.q.p, at + h * g.q.hs + d0, r);
       load8<DT, true>(g.q.p, at + h * g.q.hs + d1, r + 8);
+      if (norm) norm_unit(r, wq, U, 1.0 / g.c.D, g.eps);
       rotate_unit(r, turn, g.inter);
       store8<DT>(g.qo.p, to + h * g.qo.hs + d0, r);
       store8<DT>(g.qo.p, to + h * g.qo.hs + d1, r + 8);
@@ -370,8 +301,10 @@ __device__ void rotate_queries(const KvAppendArgs& g, int64_t row0, int64_t pos0
 }
 
 // grid: x = pages that a sequence's new tokens may touch, y = key heads,
-// value heads, then groups of query heads, z = sequences
-template <int DT>
+// value heads, then groups of query heads, z = sequences. NORM: the norm of
+// keys or queries, or both (a kernel of its own: without it the other's
+// registers and results stay as they are).
+template <int DT, bool NORM>
 __global__ __launch_bounds__(MAX_THREADS) void append_kernel(KvAppendArgs g, int q_group) {
   __shared__ float lds[MAX_THREADS / 64];
   const int b = blockIdx.z, H = g.c.heads, page = g.c.page;
@@ -390,7 +323,7 @@ __global__ __launch_bounds__(MAX_THREADS) void append_kernel(KvAppendArgs g, int
   const int rotated = (int)max((int64_t)0, known - first);   // of the n tokens
   if (role >= 2 * H) {
     const int h0 = (role - 2 * H) * q_group;
-    rotate_queries<DT>(g, row0, first, n, rotated, h0, min(g.q_heads, h0 + q_group));
+    rotate_queries<DT, NORM>(g, row0, first, n, rotated, h0, min(g.q_heads, h0 + q_group));
     return;
   }
   const int64_t id = slot < g.t.width ? g.t.table[b * g.t.width + slot] : -1;
@@ -402,7 +335,7 @@ __global__ __launch_bounds__(MAX_THREADS) void append_kernel(KvAppendArgs g, int
   if (!rotated) return;
   int bad = 0;
   const int p0 = (int)(first - slot * page);
-  if (role < H) append_keys<DT>(g, row0, first, p0, rotated, id, role, lds, &bad);
+  if (role < H) append_keys<DT, NORM>(g, row0, first, p0, rotated, id, role, lds, &bad);
   else append_values<DT>(g, row0, p0, rotated, id, role - H, lds, &bad);
   if (g.bad && bad) atomicAdd(g.bad, bad);
 }
@@ -488,9 +421,15 @@ hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st) {
   const dim3 grid(page_slots(g.t.max_tokens, g.c.page), 2 * g.c.heads + (g.q.p ? (g.q_heads + q_group - 1) / q_group : 0),
                   g.t.batch);
   const int threads = block_threads(g.t, g.c);
-  if (g.dtype == DT_F16) append_kernel<DT_F16><<<grid, threads, 0, st>>>(g, q_group);
-  else if (g.dtype == DT_BF16) append_kernel<DT_BF16><<<grid, threads, 0, st>>>(g, q_group);
-  else append_kernel<DT_F32><<<grid, threads, 0, st>>>(g, q_group);
+  if (g.k_norm || g.q_norm) {
+    if (g.dtype == DT_F16) append_kernel<DT_F16, true><<<grid, threads, 0, st>>>(g, q_group);
+    else if (g.dtype == DT_BF16) append_kernel<DT_BF16, true><<<grid, threads, 0, st>>>(g, q_group);
+    else append_kernel<DT_F32, true><<<grid, threads, 0, st>>>(g, q_group);
+  } else {
+    if (g.dtype == DT_F16) append_kernel<DT_F16, false><<<grid, threads, 0, st>>>(g, q_group);
+    else if (g.dtype == DT_BF16) append_kernel<DT_BF16, false><<<grid, threads, 0, st>>>(g, q_group);
+    else append_kernel<DT_F32, false><<<grid, threads, 0, st>>>(g, q_group);
+  }
   return hipGetLastError();
 }
 

@@ -417,6 +417,142 @@ int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_tabl
                          const float* cos, const float* sin, int64_t rot, int64_t rope_rows, int32_t interleaved,
                          int32_t* bad_count, void* stream);
 
+/* lowbit_kv_append with the norm of each head of the queries and keys before
+ * their rotation: a row x of head_dim values becomes
+ *   x / sqrt(mean x^2 + eps) * w
+ * with the weights w of its operand, then its rotation, scale and codes as
+ * above. The squares and their sum are FP64, the rest FP32 (one rounding to
+ * `dtype` for the queries, as above): within 2^-21 of the row's largest
+ * normalised value (times the largest |(cos, sin)|, 1 in plain tables) before that. A row that holds a NaN becomes NaN, one with an infinity NaN
+ * there and 0 elsewhere; a row of zeros with eps = 0 stays zeros.
+ *   q_norm, k_norm  [head_dim] of norm_dtype (F16, BF16, F32), 16-byte aligned;
+ *                   each nullable: no norm of that operand (both NULL with
+ *                   norm_dtype NONE: lowbit_kv_append). q_norm needs q.
+ *   eps             finite, >= 0; read when there is a norm */
+int32_t lowbit_kv_append_norm(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                              const int32_t* cu_tokens, const int32_t* starts, int64_t batch, int64_t tokens,
+                              int64_t max_tokens, int32_t dtype,
+                              const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                              const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                              const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                              void* q_out, int64_t qo_token_stride, int64_t qo_head_stride,
+                              const float* cos, const float* sin, int64_t rot, int64_t rope_rows, int32_t interleaved,
+                              const void* q_norm, const void* k_norm, int32_t norm_dtype, float eps,
+                              int32_t* bad_count, void* stream);
+
+/* The same norm and rotation of dense queries and keys, without a cache (as
+ * the image and text tokens of a diffusion transformer's blocks need them):
+ * token t's rows are normalised, rotated by position positions[t] (t itself
+ * where positions is NULL) and rounded once. Tokens whose position is not in
+ * the tables become zeros and are counted in bad_count[0].
+ *   q, k           [tokens][heads][head_dim] of dtype (F16, BF16, F32); k is
+ *                  nullable, with k_out. Strides and alignment as in
+ *                  lowbit_kv_append; q_out and k_out may be q and k themselves
+ *                  with the same strides
+ *   head_dim       64, 128 or 256; heads 1 .. 65536
+ *   q_norm, k_norm as in lowbit_kv_append_norm, each nullable (no norm)
+ *   cos, sin, rot  as in lowbit_kv_append; NULL with rot = 0 (no rotation; then
+ *                  there is a norm)
+ *   positions      nullable int32 [tokens]
+ *   bad_count      nullable device int32[1], added to */
+int32_t lowbit_norm_rotate(int32_t dtype, int64_t tokens, int64_t head_dim,
+                           const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                           void* q_out, int64_t qo_token_stride, int64_t qo_head_stride,
+                           const void* k, int64_t k_token_stride, int64_t k_head_stride, int64_t k_heads,
+                           void* k_out, int64_t ko_token_stride, int64_t ko_head_stride,
+                           const void* q_norm, const void* k_norm, int32_t norm_dtype, float eps,
+                           const float* cos, const float* sin, int64_t rot, int64_t rope_rows,
+                           const int32_t* positions, int32_t interleaved, int32_t* bad_count, void* stream);
+
+/* Tables for the rotation: cos[p][i] = m cos((first + p) f_i), sin alike, for
+ * p < positions and i < rot / 2, FP32 and contiguous, 16-byte aligned.
+ * Frequencies are f_i = base^(-2 i / rot), scaled for contexts longer than the
+ * `original` length that a model was trained on:
+ *   PLAIN       as they are
+ *   LINEAR      f_i / factor
+ *   NTK         with base * factor^(rot / (rot - 2)) for base
+ *   YARN        f_i (1 - r) + f_i / factor r, with r rising from 0 to 1 over the
+ *               dimensions i between those that make `high` and `low` turns over
+ *               `original` (rot log(original / (2 pi turns)) / (2 log base),
+ *               rounded outwards, within 0 .. rot - 1)
+ *   WAVELENGTH  the same sum with r falling linearly from 1 to 0 over the turns
+ *               original f_i / (2 pi) between `low` and `high`
+ * (YARN: Peng, Quesnelle, Fan, Shippole, "YaRN: Efficient Context Window
+ * Extension of Large Language Models", 2023; LINEAR and NTK as described there.)
+ * Frequencies and angles are FP64; entries are within m (2^-21 + 2^-50 position)
+ * of the exact ones.
+ *   rot        32 .. 256, a multiple of 32
+ *   positions  >= 0, first >= 0, first + positions <= 2^31
+ *   base       > 1; factor >= 1; original > 0, 0 < low < high (YARN, WAVELENGTH)
+ *   magnitude  m; 0 for the rule's own: 0.1 log(factor) + 1 with YARN, else 1 */
+typedef enum { LOWBIT_ROPE_PLAIN = 0, LOWBIT_ROPE_LINEAR = 1, LOWBIT_ROPE_NTK = 2, LOWBIT_ROPE_YARN = 3,
+               LOWBIT_ROPE_WAVELENGTH = 4 } lowbit_rope_scaling;
+int32_t lowbit_rope_tables(float* cos, float* sin, int64_t positions, int64_t rot, int64_t first, double base,
+                           int32_t scaling, double factor, double original, double low, double high, double magnitude,
+                           void* stream);
+
+/* A new table of pages for the sequences that go on, worked out on the device:
+ * forking, reordering, dropping and trimming sequences, letting go of pages that
+ * a window has passed, making room for the next tokens, and moving the used
+ * pages to the front of the pool.
+ *   New sequence c continues old sequence rows[c] (c itself where rows is NULL;
+ * a number outside 0 .. batch - 1 begins an empty sequence) with its L_c =
+ * lens[rows[c]] tokens, counted as at most what a row of either table holds and
+ * at least 0. It keeps the pages of these tokens, but (window > 0) those whose
+ * tokens are all behind the first `sinks` and out of sight of position L_c
+ * (t <= L_c - window); entries that are no page stay none.
+ *   The last page of a sequence, where its tokens fill it in part, is the next
+ * tokens' page too, is always kept, and becomes the sequence's own: the lowest c
+ * keeps it unless another sequence keeps it as a whole page; the others get a
+ * page for a copy. Slots for room[c] more tokens (none where room is NULL) get
+ * pages as well, up to new_width. Pages that no new sequence keeps are free; the
+ * lowest of them are taken, in the order of c, then slots. Where they run out
+ * the remaining slots become -1 and are counted (a copy that finds no page loses
+ * the page's tokens).
+ *   compact: of the n pages then in use, those numbered n and more move to free
+ * ones below n, the lowest to the lowest, before the other needs take theirs.
+ *   The pairs (src[i], dst[i]) say which pages to copy, in every layer's cache,
+ * with lowbit_kv_copy_pages: first the moves, then the copies of the last pages
+ * in the order of c; the rest of the lists becomes -1. No destination is a
+ * source or a destination twice, so the pairs have no order.
+ *   The new table holds nothing but the new sequences: a sequence that is to
+ * live on has to be among the rows. Everything is a function of the arguments.
+ *   block_table  int32 [batch][table_width], lens int32 [batch]: batch 0 .. 65535
+ *   pages, page  of the cache
+ *   rows, room   nullable int32 [new_batch], new_batch 0 .. 65535 (rows NULL:
+ *                new_batch = batch)
+ *   new_table    int32 [new_batch][new_width]; new_lens int32 [new_batch]: L_c.
+ *                new_batch * max(table_width, new_width) < 2^31
+ *   src, dst     int32 [pairs], pairs >= lowbit_kv_remap_pairs()
+ *   counts       int32 [4]: pairs, pages in use afterwards, slots that found no
+ *                page, moves among the pairs
+ *   workspace    lowbit_kv_remap_workspace_bytes() bytes, 256-byte aligned; no
+ *                initialisation; calls that can run concurrently must not share it
+ * All arrays are on the device, 4-byte aligned; outputs overlap nothing. */
+int32_t lowbit_kv_remap(const int32_t* block_table, int64_t table_width, const int32_t* lens, int64_t batch,
+                        int64_t pages, int32_t page, const int32_t* rows, const int32_t* room, int64_t new_batch,
+                        int64_t window, int64_t sinks, int32_t compact,
+                        int32_t* new_table, int64_t new_width, int32_t* new_lens,
+                        int32_t* src, int32_t* dst, int64_t pairs, int32_t* counts,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* The least `pairs` of lowbit_kv_remap (new_batch, and min(pages / 2, new_batch
+ * * table_width) more with compact); -1 for a bad shape. */
+int64_t lowbit_kv_remap_pairs(int64_t table_width, int64_t new_batch, int64_t pages, int32_t compact);
+
+/* Workspace bytes lowbit_kv_remap needs (0 for a bad shape). */
+size_t lowbit_kv_remap_workspace_bytes(int64_t new_batch, int64_t pages);
+
+/* Copy whole pages inside a cache: page dst[i] becomes page src[i] (keys,
+ * values and scales of all heads) for i < pairs, or i < count[0] where count is
+ * given (a device int32, taken as 0 .. pairs: no host waits for it). Pairs with
+ * a number outside 0 .. pages - 1, or with src = dst, are left out. The pairs
+ * are copied at the same time: a page that is the destination of two different
+ * sources, or a source as well as a destination, ends up with bytes of either.
+ *   src, dst   int32 [pairs] on the device, 4-byte aligned; pairs >= 0 */
+int32_t lowbit_kv_copy_pages(const lowbit_kv_cache* cache, const int32_t* src, const int32_t* dst, int64_t pairs,
+                             const int32_t* count, void* stream);
+
 /* The inverse: rows cu_tokens[b] .. cu_tokens[b+1] - 1 of k and v
  * ([tokens][kv_heads][head_dim] of `dtype`, strides as q_out above) become the
  * values that the cache holds for sequence b's tokens starts[b], starts[b] + 1,
@@ -474,6 +610,25 @@ int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_tabl
  * and the current device's CU count (256 when no gfx950 device is current). */
 size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
                                         int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window);
+
+/* lowbit_attention with first tokens that stay visible beside the window: token
+ * j is seen when j < lens[b], j <= position (causal not 0), its page exists,
+ * and j > position - window or j < sinks. Without a window (0) every token is
+ * seen as before. Tokens between are not read: their pages may have gone back
+ * to the pool (table entries of -1). Everything else, workspace included, as
+ * lowbit_attention with lowbit_attention_sinks_workspace_bytes.
+ *   sinks   >= 0; any number */
+int32_t lowbit_attention_sinks(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
+                               const int32_t* cu_tokens, const int32_t* lens, int64_t batch, int64_t tokens,
+                               int64_t max_tokens, int64_t max_len, int32_t dtype,
+                               const void* q, int64_t q_token_stride, int64_t q_head_stride, int64_t q_heads,
+                               void* out, int64_t o_token_stride, int64_t o_head_stride, float* lse,
+                               float scale, int32_t causal, int64_t window, int64_t sinks,
+                               void* workspace, size_t workspace_bytes, void* stream);
+
+size_t lowbit_attention_sinks_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
+                                              int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window,
+                                              int64_t sinks);
 
 /* Several independent linears of one shape in one launch: problem z computes
  *
