@@ -39,6 +39,7 @@ __device__ __forceinline__ void put(T* p, T v) {
 // [grow0, grow1) that its room takes beyond them.
 struct Row {
   int64_t at;               // of the old row in the old table
+  int row;                  // the old row, 0 where there is none
   int len, part;            // part: the slot of a partly filled last page, -1 where there is none
   int grow0, grow1;
 };
@@ -47,7 +48,8 @@ __device__ __forceinline__ Row find_row(const RemapArgs& g, int c) {
   const int r = g.rows ? g.rows[c] : c;
   Row w;
   const bool goes = r >= 0 && r < g.batch;
-  w.at = goes ? (int64_t)r * g.width : 0;
+  w.row = goes ? r : 0;
+  w.at = w.row * g.width;
   w.len = goes ? max(0, min(g.lens[r], g.most)) : 0;
   const int whole = w.len >> g.shift, rest = w.len & (g.page - 1);
   w.part = rest ? whole : -1;
@@ -98,27 +100,37 @@ __device__ void mark(const RemapArgs& g, int64_t tid, int64_t threads) {
   }
 }
 
-// What a thread's value adds to before it, and the workgroup's total.
+// The sum of x over the lanes up to this one, by DPP moves: within rows of 16
+// lanes, then the last lane of a row to the next row, and of two rows to the others.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int moved(int x) { return __builtin_amdgcn_update_dpp(0, x, CTRL, ROWS, 0xf, false); }
+__device__ __forceinline__ int row_sums(int x) {
+  x += moved<0x111, 0xf>(x);
+  x += moved<0x112, 0xf>(x);
+  x += moved<0x114, 0xf>(x);
+  return x + moved<0x118, 0xf>(x);
+}
+__device__ __forceinline__ int wave_sums(int x) {
+  x = row_sums(x);
+  x += moved<0x142, 0xa>(x);
+  return x + moved<0x143, 0xc>(x);
+}
+
+// What a thread's values add to before it, and the workgroup's totals (of 16 waves).
 __device__ __forceinline__ int2 scan2(int2 v, int2* lds, int2* total) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int2 x = v;
-#pragma unroll
-  for (int i = 1; i < 64; i <<= 1) {
-    const int a = __shfl_up(x.x, i), b = __shfl_up(x.y, i);
-    if (lane >= i) x.x += a, x.y += b;
-  }
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int2 x = {wave_sums(v.x), wave_sums(v.y)};
   if (lane == 63) lds[wave] = x;
   __syncthreads();
-  int2 before = {0, 0}, all = {0, 0};
-  for (int k = 0; k < SCAN_THREADS / 64; ++k) {
-    const int2 y = lds[k];
-    if (k < wave) before.x += y.x, before.y += y.y;
-    all.x += y.x, all.y += y.y;
-  }
+  int2 y = lds[lane & 15];                                   // every row of 16 lanes holds the 16 waves' sums
+  y = {row_sums(y.x), row_sums(y.y)};
   __syncthreads();
-  *total = all;
-  return {before.x + x.x - v.x, before.y + x.y - v.y};
+  *total = {__builtin_amdgcn_readlane(y.x, 15), __builtin_amdgcn_readlane(y.y, 15)};
+  const int before = max(wave - 1, 0);
+  const int2 base = {__builtin_amdgcn_readlane(y.x, before), __builtin_amdgcn_readlane(y.y, before)};
+  return {(wave ? base.x : 0) + x.x - v.x, (wave ? base.y : 0) + x.y - v.y};
 }
+static_assert(SCAN_THREADS == 16 * 64, "one row of lanes holds the waves' sums");
 
 __device__ __forceinline__ int rank_of(const RemapArgs& g, int p) {   // used pages below p
   if (p >= g.pages) return g.info->used;
@@ -169,14 +181,10 @@ __device__ void scan(const RemapArgs& g) {
   if (mine) atomicAdd(&done, mine);
   // the lowest free pages: the first `moves` of them take the pages that move
   const int take = moves + fresh;
-  for (int64_t i = tid; i < g.words; i += SCAN_THREADS) {
-    int at = (int)(32 * i) - g.before[i];
-    if (at >= take) break;                                   // free pages before a word never get fewer
-    uint32_t free = ~get(g.used + i);
-    for (; free && at < take; free &= free - 1, ++at) {
-      const int64_t p = 32 * i + __ffs(free) - 1;
-      if (p < g.pages) g.free[at] = (int)p;
-    }
+  for (int64_t p = tid; p < g.pages; p += SCAN_THREADS) {
+    const int at = (int)p - rank_of(g, (int)p);
+    if (at >= take) break;                                   // free pages before a page never get fewer
+    if (!(get(g.used + (p >> 5)) >> (p & 31) & 1)) g.free[at] = (int)p;
   }
   __syncthreads();
   if (tid == 0) {
@@ -218,14 +226,11 @@ __device__ void apply(const RemapArgs& g, int64_t tid, int64_t threads) {
   if (!wide)
     for (int64_t c = tid; c < g.new_batch; c += threads) g.lens_out[c] = 0;
   if (moves) {
-    for (int64_t i = (n >> 5) + tid; i < g.words; i += threads) {
-      uint32_t bits = get(g.used + i);
-      if (i == n >> 5) bits &= ~((1u << (n & 31)) - 1u);
-      for (; bits; bits &= bits - 1) {
-        const int p = (int)(32 * i) + __ffs(bits) - 1, k = rank_of(g, p) - below;
-        g.src[k] = p;
-        g.dst[k] = g.free[k];
-      }
+    for (int64_t p = n + tid; p < g.pages; p += threads) {
+      if (!(get(g.used + (p >> 5)) >> (p & 31) & 1)) continue;
+      const int k = rank_of(g, (int)p) - below;
+      g.src[k] = (int)p;
+      g.dst[k] = g.free[k];
     }
   }
   for (int64_t i = pairs + tid; i < g.capacity; i += threads) g.src[i] = g.dst[i] = -1;
@@ -242,15 +247,207 @@ __global__ __launch_bounds__(256) void remap_apply_kernel(RemapArgs g) {
   apply(g, (int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256);
 }
 
-// All steps by one workgroup, for small tables.
-__global__ __launch_bounds__(SCAN_THREADS) void remap_kernel(RemapArgs g) {
-  clear(g, threadIdx.x, SCAN_THREADS);
+// The steps by one workgroup with the sets and the rows in LDS, the last one
+// (APPLY) for small tables only. Bound by latency (rows, lengths and table one
+// after the other, then the table again for the new one) and, for larger tables,
+// by the instructions of one CU: a power of two of lanes, as wide as a row or 64,
+// walks the slots of a row, so that there is no division, with BATCH entries in
+// flight.
+constexpr int BATCH = 4;
+
+// The slots of rows c, c + step, ... that a thread takes: s0, s0 + lanes, ... of
+// each. WIDE: 64 lanes a row, whose number and values are the same in all of a wave.
+template <bool WIDE>
+struct Walk {
+  int c, s, wide, step, s0, lanes;
+  __device__ __forceinline__ Walk(int slots, int log_lanes) {
+    if (WIDE) log_lanes = 6;
+    lanes = 1 << log_lanes;
+    s0 = threadIdx.x & (lanes - 1);
+    s = 0;
+    c = threadIdx.x >> log_lanes;
+    if (WIDE) c = __builtin_amdgcn_readfirstlane(c);
+    step = SCAN_THREADS >> log_lanes;
+    wide = slots;
+  }
+  __device__ __forceinline__ bool any(int R) const { return c < R && wide; }
+  __device__ __forceinline__ int slot() const { return s + s0; }    // at or past `wide`: none
+  __device__ __forceinline__ void next() {
+    s += lanes;
+    if (s >= wide) s = 0, c += step;
+  }
+};
+
+struct LdsRow {
+  int src, full, gone1;     // old row; slots that its tokens fill; those from gone0 to here the window has passed
+  int grow0, grow1;         // slots of its room; a partly filled one is `full`, before grow0
+  int id;                   // the page of that one, -1 where there is none
+  int need, copy;           // new pages of the rows before; the row's copy among all, or -1
+};
+struct Sets {
+  uint32_t* used;
+  uint32_t* whole;
+  int* before;
+  __device__ __forceinline__ bool has(int p) const { return used[p >> 5] >> (p & 31) & 1; }
+  __device__ __forceinline__ int rank(int p) const { return before[p >> 5] + __popc(used[p >> 5] & ((1u << (p & 31)) - 1u)); }
+};
+
+size_t remap_lds(int64_t new_batch, int64_t words) { return 12 * words + sizeof(LdsRow) * new_batch; }
+
+template <bool WIDE, bool APPLY>
+__global__ __launch_bounds__(SCAN_THREADS) void remap_kernel(RemapArgs g, int log_lanes) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ int2 lds[SCAN_THREADS / 64];
+  __shared__ int done;
+  const int tid = threadIdx.x, R = g.new_batch, pages = (int)g.pages, words = (int)g.words;
+  LdsRow* const rows = (LdsRow*)smem;
+  const Sets set = {(uint32_t*)(rows + R), (uint32_t*)(rows + R) + words, (int*)(rows + R) + 2 * words};
+  for (int i = tid; i < words; i += SCAN_THREADS) set.used[i] = set.whole[i] = 0;
+  if (tid == 0) done = 0;
+  for (int c = tid; c < R; c += SCAN_THREADS) {
+    const Row w = find_row(g, c);
+    const int id = w.part >= 0 ? kept(g, w, w.part) : -1;
+    if (id >= 0) put(g.owner + id, 0x7fffffff);
+    // slot s is passed when (s + 1) page - 1 <= len - window
+    const int64_t passed = g.window ? (int64_t)w.len - g.window + 1 : 0;
+    rows[c] = {w.row, w.len >> g.shift, passed > 0 ? (int)(passed >> g.shift) : 0, w.grow0, w.grow1, id, 0, 0};
+    put(g.lens_out + c, w.len);
+  }
   __syncthreads();
-  mark(g, threadIdx.x, SCAN_THREADS);
+
+  // the page of slot s of row c, where its tokens fill it and it is kept: no branches, so that the loads do not wait
+  // for each other; what is not there is read at the first entry (of any array, where the table has none)
+  const int gone0 = (int)min((g.sinks + g.page - 1) >> g.shift, (int64_t)0x7fffffff);
+  const int32_t* const table = g.batch && g.width ? g.table : g.counts;
+  auto entry = [&](int c, int s) __attribute__((always_inline)) {
+    const LdsRow& r = rows[min(c, R - 1)];
+    int src = r.src, full = r.full, gone1 = r.gone1;
+    if (WIDE) {
+      src = __builtin_amdgcn_readfirstlane(src);
+      full = __builtin_amdgcn_readfirstlane(full);
+      gone1 = __builtin_amdgcn_readfirstlane(gone1);
+    }
+    const bool go = (c < R) & (s < full) & ((s < gone0) | (s >= gone1));
+    const int id = table[go ? (int64_t)src * g.width + s : 0];
+    return (go & (id >= 0) & (id < pages)) ? id : -1;
+  };
+  for (int c = tid; c < R; c += SCAN_THREADS) {
+    const int id = rows[c].id;
+    if (id < 0) continue;
+    atomicOr(&set.used[id >> 5], 1u << (id & 31));
+    __hip_atomic_fetch_min(g.owner + id, c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  const int slots = (int)min(g.width, g.width_out), wide = (int)g.width_out;
+  for (Walk<WIDE> w(slots, log_lanes); w.any(R);) {
+    int id[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k, w.next()) id[k] = entry(w.c, w.slot());
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      if (id[k] < 0) continue;
+      atomicOr(&set.used[id[k] >> 5], 1u << (id[k] & 31));
+      atomicOr(&set.whole[id[k] >> 5], 1u << (id[k] & 31));
+    }
+  }
   __syncthreads();
-  scan(g);
+
+  int2 total, run = {0, 0};
+  for (int b = 0; b < words; b += SCAN_THREADS) {
+    const int i = b + tid;
+    const int2 mine = {i < words ? __popc(set.used[i]) : 0, 0};
+    const int2 at = scan2(mine, lds, &total);
+    if (i < words) set.before[i] = run.x + at.x;
+    run.x += total.x;
+  }
+  const int used = run.x;
+  run = {0, 0};
+  for (int b = 0; b < R; b += SCAN_THREADS) {
+    const int c = b + tid;
+    int2 mine = {0, 0};
+    if (c < R) {
+      const LdsRow& r = rows[c];
+      mine.y = r.id >= 0 && ((set.whole[r.id >> 5] >> (r.id & 31) & 1) || get(g.owner + r.id) != c);
+      mine.x = mine.y + r.grow1 - r.grow0;
+    }
+    const int2 at = scan2(mine, lds, &total);
+    if (c < R) {
+      rows[c].need = run.x + at.x;
+      rows[c].copy = mine.y ? run.y + at.y : -1;
+    }
+    run.x += total.x;
+    run.y += total.y;
+  }
+  const int need = run.x, fresh = min(need, pages - used), n = used + fresh;
+  int copies = run.y;
+  if (fresh < need) {                                        // those of rows whose turn comes before the free pages run out
+    int mine = 0;
+    for (int c = tid; c < R; c += SCAN_THREADS) mine += rows[c].copy >= 0 && rows[c].need < fresh;
+    if (mine) atomicAdd(&done, mine);
+    __syncthreads();
+    copies = done;
+  }
+  const int below = n < pages ? set.rank(n) : used, moves = g.compact ? used - below : 0, pairs = moves + copies;
+  for (int p = tid; p < pages; p += SCAN_THREADS) {          // the lowest free pages
+    const int at = p - set.rank(p);
+    if (at >= moves + fresh) break;                          // free pages before a page never get fewer
+    if (!set.has(p)) g.free[at] = p;
+  }
+  if (tid < 4) g.counts[tid] = tid == 0 ? pairs : tid == 1 ? n : tid == 2 ? need - fresh : moves;
+  if (!APPLY) {                                              // what the last step reads
+    if (tid == 0) *g.info = {used, fresh, n, moves, pairs};
+    for (int c = tid; c < R; c += SCAN_THREADS) {
+      g.need[c] = rows[c].need;
+      g.copy[c] = rows[c].copy;
+    }
+    if (moves) {
+      for (int i = tid; i < words; i += SCAN_THREADS) {
+        g.used[i] = set.used[i];
+        g.before[i] = set.before[i];
+      }
+    }
+    return;
+  }
   __syncthreads();
-  apply(g, threadIdx.x, SCAN_THREADS);
+
+  for (Walk<WIDE> w(wide, log_lanes); w.any(R);) {
+    Walk<WIDE> v = w;
+    int id[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k, w.next()) id[k] = entry(w.c, w.slot());
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k, v.next()) {
+      const int s = v.slot();
+      if (v.c >= R || s >= wide) continue;
+      const LdsRow& r = rows[v.c];
+      int to = id[k];
+      if (s >= r.full && s < r.grow1) {                      // the partly filled slot, and the room's
+        const bool copy = s < r.grow0 && r.copy >= 0;
+        if (s < r.grow0) to = r.id;
+        if (copy || s >= r.grow0) {
+          const int nth = copy ? r.need : r.need + (r.copy >= 0) + s - r.grow0;
+          to = nth < fresh ? g.free[moves + nth] : -1;
+          if (copy && to >= 0) {
+            g.src[moves + r.copy] = r.id;
+            g.dst[moves + r.copy] = to;
+          }
+        } else if (moves && to >= n) {
+          to = g.free[set.rank(to) - below];
+        }
+      } else if (moves && to >= n) {
+        to = g.free[set.rank(to) - below];
+      }
+      g.table_out[v.c * g.width_out + s] = to;
+    }
+  }
+  if (moves) {
+    for (int p = n + tid; p < pages; p += SCAN_THREADS) {
+      if (!set.has(p)) continue;
+      const int k = set.rank(p) - below;
+      g.src[k] = p;
+      g.dst[k] = g.free[k];
+    }
+  }
+  for (int64_t i = pairs + tid; i < g.capacity; i += SCAN_THREADS) g.src[i] = g.dst[i] = -1;
 }
 
 // A pair's blocks (all heads of a page lie together) in pieces of PIECE bytes,
@@ -286,6 +483,13 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(KvCache c, const int32_
   }
 }
 
+// One launch up to APPLY_SLOTS slots (4032: 8.4 us, 8.6 in two; 1216: 6.5 and 8.1;
+// 8064: 11.0 and 9.0), two up to SCAN_SLOTS (20032: 12.2 us, 15.2 in four; 37800:
+// 17.7 and 18.6; 64064: 23.7 and 18.1), four beyond or where the rows and the sets
+// do not fit the LDS of ONE_LDS bytes.
+constexpr int64_t APPLY_SLOTS = 4096, SCAN_SLOTS = 32768;
+constexpr size_t ONE_LDS = 56 << 10;
+
 size_t up(size_t bytes) { return (bytes + 255) / 256 * 256; }
 
 }  // namespace
@@ -312,15 +516,23 @@ hipError_t launch_remap(RemapArgs g, void* workspace, int num_cu, hipStream_t st
   g.need = (int32_t*)take(4 * g.new_batch);
   g.copy = (int32_t*)take(4 * g.new_batch);
   const int64_t slots = g.new_batch * std::max(g.width_out, g.width);
-  if (slots <= 16384 && g.pages <= 65536) {
-    remap_kernel<<<1, SCAN_THREADS, 0, st>>>(g);
+  auto blocks = [&](int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 8 * num_cu)); };
+  const size_t lds = remap_lds(g.new_batch, g.words);
+  if (slots <= SCAN_SLOTS && lds <= ONE_LDS) {
+    int log_lanes = 2;
+    while (log_lanes < 6 && g.width_out >> log_lanes) ++log_lanes;
+    const bool apply = slots <= APPLY_SLOTS;
+    if (log_lanes == 6 && apply) remap_kernel<true, true><<<1, SCAN_THREADS, lds, st>>>(g, 6);
+    else if (log_lanes == 6) remap_kernel<true, false><<<1, SCAN_THREADS, lds, st>>>(g, 6);
+    else if (apply) remap_kernel<false, true><<<1, SCAN_THREADS, lds, st>>>(g, log_lanes);
+    else remap_kernel<false, false><<<1, SCAN_THREADS, lds, st>>>(g, log_lanes);
+    if (!apply) remap_apply_kernel<<<blocks(std::max(slots, g.pages)), 256, 0, st>>>(g);
     return hipGetLastError();
   }
-  auto blocks = [&](int64_t n) { return (unsigned)std::max<int64_t>(1, std::min<int64_t>((n + 255) / 256, 8 * num_cu)); };
   remap_clear_kernel<<<blocks(std::max(g.words, (int64_t)g.new_batch)), 256, 0, st>>>(g);
   remap_mark_kernel<<<blocks(slots), 256, 0, st>>>(g);
   remap_scan_kernel<<<1, SCAN_THREADS, 0, st>>>(g);
-  remap_apply_kernel<<<blocks(std::max(slots, g.words)), 256, 0, st>>>(g);
+  remap_apply_kernel<<<blocks(std::max(slots, g.pages)), 256, 0, st>>>(g);
   return hipGetLastError();
 }
 

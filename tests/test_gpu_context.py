@@ -517,8 +517,8 @@ def test_kv_remap_by_default_keeps_everything(lb):
 
 @pytest.mark.parametrize("compact", [False, True])
 def test_kv_remap_of_large_tables(lb, compact):
-    """Tables and pools beyond what one workgroup takes: the steps as launches of their own."""
-    banner(f"remap of 300 x 300, compact {compact}")
+    """Tables and pools at the end of what one workgroup takes, and beyond: the steps as launches of their own."""
+    banner(f"remap of 300 x 100, compact {compact}")
     g = np.random.default_rng(60)
     table, lens = _random_tables(g, 300, 100, 40000, 16, 20, 0.01)
     rows = np.concatenate([g.permutation(300)[:170], g.integers(0, 300, 30), [-1, 300]])
@@ -528,6 +528,14 @@ def test_kv_remap_of_large_tables(lb, compact):
     _remap_check(lb, table[:3], lens[:3], 70000, 16, rows=np.array([2, 2, 0]), room=np.array([50, 0, 7]), compact=compact)
     table, lens = _random_tables(g, 300, 100, 17000, 16, 0, 0.0)
     _remap_check(lb, table, lens, 17000, 16, rows=g.integers(0, 300, 2000), room=np.full(2000, 200), compact=compact)
+    # more slots than one workgroup takes, with common pages, a window and entries that are no page
+    table, lens = _random_tables(g, 300, 100, 40000, 16, 20, 0.01)
+    rows = g.integers(-1, 301, 900)
+    _remap_check(lb, table, lens, 40000, 16, rows=rows, room=g.integers(-9, 90, 900), window=900, sinks=40, compact=compact,
+                 width=110)
+    # more pages than its sets hold
+    _remap_check(lb, table[:50], lens[:50], 170000, 16, rows=rows[:60], room=g.integers(0, 90, 60), window=500, compact=compact,
+                 cache=Pool(lb, 170000, 16, 1))
 
 
 def test_kv_remap_of_nothing(lb):
