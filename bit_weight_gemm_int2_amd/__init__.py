@@ -81,7 +81,7 @@ SIGNATURES = [
     ("lowbit_kv_copy_pages", _I32, [_P, _P, _P, _I64, _P, _P]),
     ("lowbit_attention_sinks", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64,
                                       _P, _I64, _I64, _P, ctypes.c_float, _I32, _I64, _I64, _P, _SZ, _P]),
-    ("lowbit_attention_sinks_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64, _I64]),
+    ("lowbit_attention_sinks_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I32, _I64, _I64]),
     ("lowbit_quantize", _I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
 ]
 MAX_GROUP = 8
@@ -798,7 +798,7 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
     lse = _new((T, Hq), torch.float32, q, stream) if return_lse else None
     L = lib()
     if sinks:
-        need = L.lowbit_attention_sinks_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window, sinks)
+        need = L.lowbit_attention_sinks_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, causal, window, sinks)
     else:
         need = L.lowbit_attention_workspace_bytes(head[4], T, max_tokens, max_len, Hq, H, D, window)
     size = 0

@@ -34,7 +34,7 @@ hipError_t launch_kv_append(const KvAppendArgs& g, hipStream_t st);
 hipError_t launch_kv_read(const KvReadArgs& g, hipStream_t st);
 hipError_t launch_attention(const AttnArgs& a, AttnPlan p, hipStream_t st);
 AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
-                        int D, int num_cu);
+                        bool causal, int D, int num_cu);
 hipError_t launch_norm_rotate(const TurnArgs& g, hipStream_t st);
 hipError_t launch_rope_tables(const TableArgs& g, hipStream_t st);
 size_t remap_workspace(int64_t new_batch, int64_t pages);
@@ -783,7 +783,7 @@ size_t attention_bytes(int splits, int64_t tokens, int64_t q_heads, int64_t D) {
 }
 
 size_t attention_workspace(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len, int64_t q_heads,
-                           int64_t kv_heads, int64_t head_dim, int64_t window, int64_t sinks) {
+                           int64_t kv_heads, int64_t head_dim, bool causal, int64_t window, int64_t sinks) {
   if (batch < 1 || tokens < 1 || max_tokens < 1 || max_len < 0 || kv_heads < 1 || q_heads < kv_heads || window < 0 ||
       sinks < 0 ||      batch > 65535 || tokens >= kMaxDim || q_heads > 65536 || max_len > ((int64_t)1 << 30))
     return 0;
@@ -791,8 +791,8 @@ size_t attention_workspace(int64_t batch, int64_t tokens, int64_t max_tokens, in
   if (current_device(&num_cu) != LOWBIT_OK) num_cu = 256;   // no gfx950 device: the MI355X's count
   const lowbit::AttnPlan p =
       lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
-                             (int)std::min(window, max_len), window ? (int)std::min(sinks, max_len) : 0, (int)head_dim,
-                             num_cu);
+                             (int)std::min(window, max_len), window ? (int)std::min(sinks, max_len) : 0, causal,
+                             (int)head_dim, num_cu);
   return attention_bytes(p.splits, tokens, q_heads, head_dim);
 }
 
@@ -845,7 +845,7 @@ int32_t attention(const lowbit_kv_cache* cache, const int32_t* block_table, int6
   a.sinks = window ? (int)std::min(sinks, max_len) : 0;
   a.max_len = (int)max_len;
   const lowbit::AttnPlan p = lowbit::attention_plan(batch, (int)H, a.group, max_tokens, max_len,
-                                                    (int)std::min(window, max_len), a.sinks, (int)D, num_cu);
+                                                    (int)std::min(window, max_len), a.sinks, a.causal, (int)D, num_cu);
   a.splits = p.splits;
   a.split_len = p.split_len;
   const size_t need = attention_bytes(a.splits, tokens, q_heads, D);
@@ -902,7 +902,7 @@ int32_t lowbit_kv_read(const lowbit_kv_cache* cache, const int32_t* block_table,
 
 size_t lowbit_attention_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
                                         int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window) {
-  return attention_workspace(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, window, 0);
+  return attention_workspace(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, true, window, 0);
 }
 
 int32_t lowbit_attention(const lowbit_kv_cache* cache, const int32_t* block_table, int64_t table_width,
@@ -938,9 +938,9 @@ int32_t lowbit_attention_sinks(const lowbit_kv_cache* cache, const int32_t* bloc
 }
 
 size_t lowbit_attention_sinks_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
-                                              int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window,
-                                              int64_t sinks) {
-  return attention_workspace(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, window, sinks);
+                                              int64_t q_heads, int64_t kv_heads, int64_t head_dim, int32_t causal,
+                                              int64_t window, int64_t sinks) {
+  return attention_workspace(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, causal != 0, window, sinks);
 }
 
 int32_t lowbit_norm_rotate(int32_t dtype, int64_t tokens, int64_t head_dim, const void* q, int64_t qts, int64_t qhs,

@@ -131,6 +131,8 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int b, int row0, in
   }
   w->t0 = (int)min((int64_t)end, beg + (int64_t)split * a.split_len);
   w->t1 = (int)min((int64_t)end, beg + ((int64_t)split + 1) * a.split_len);
+  // a part behind the last token holds no place (with SINKS no token before t0 is masked, so none may be read)
+  if (SINKS && w->t0 == w->t1) w->t0 = w->t1 = w->t1 & ~15;
   w->end = SINKS && w->t1 > w->head ? w->t1 + w->skip : w->t1;
   return true;
 }
@@ -821,6 +823,51 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a) {
   if (tid == 0) store_lse(a, token, head, m, l);
 }
 
+// The same join of up to 8 parts (as many as the kernel above has groups), to the
+// bit, where there are many rows: D / 4 threads a row, every read under way at
+// once. 1024 queries of 32 heads in two parts: 87 us with their attention, 124 with
+// a workgroup a row.
+template <bool BF16, int D>
+__global__ __launch_bounds__(256) void attend_join_rows_kernel(AttnArgs a) {
+#pragma clang fp contract(off)                                         // the other kernel rounds products before it adds them
+  constexpr int TPR = D / 4, NG = 256 / TPR, MAX = NG < 8 ? NG : 8;
+  const int64_t total = a.t.tokens * a.q_heads, row = (int64_t)blockIdx.x * NG + threadIdx.x / TPR;
+  const int d = threadIdx.x % TPR * 4;
+  if (row >= total) return;
+  const f32x2* ml = (const f32x2*)(a.part + a.splits * total * D);
+  f32x2 x[8];
+  f32x4 p[MAX];
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    x[s] = f32x2{NEG_INF, 0.0f};
+    if (s < MAX && s < a.splits) x[s] = ml[s * total + row];
+  }
+#pragma unroll
+  for (int s = 0; s < MAX; ++s) {
+    p[s] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (s < a.splits && x[s][1] != 0.0f) p[s] = *(const f32x4*)(a.part + (s * total + row) * D + d);
+  }
+  float m = x[0][0];
+#pragma unroll
+  for (int s = 1; s < MAX; ++s) m = fmaxf(m, x[s][0]);
+  const float base = m > NEG_INF ? m : 0.0f;
+  float l[8];
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int s = 0; s < 8; ++s) {
+    const float f = x[s][1] != 0.0f ? __builtin_amdgcn_exp2f(x[s][0] - base) : 0.0f;
+    l[s] = x[s][1] != 0.0f ? x[s][1] * f : 0.0f;
+    if (s < MAX) v += x[s][1] != 0.0f ? f * p[s] : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  v *= inverse_sum(((l[0] + l[4]) + (l[2] + l[6])) + ((l[1] + l[5]) + (l[3] + l[7])));
+  const int64_t token = row / a.q_heads;
+  if (token < a.t.cu[0] || token >= a.t.cu[a.t.batch]) return;         // no sequence's: no part was written
+  const int head = (int)(row % a.q_heads);
+  *(u32x2*)((uint16_t*)a.o.p + token * a.o.ts + head * a.o.hs + d) = u32x2{out2<BF16>(v[0], v[1]), out2<BF16>(v[2], v[3])};
+  if (d == 0) store_lse(a, token, head, m, ((l[0] + l[4]) + (l[2] + l[6])) + ((l[1] + l[5]) + (l[3] + l[7])));
+}
+
+constexpr int JOIN_ROWS = 512;
 constexpr int FEW_ROWS = 80;
 constexpr int FEW_SPLIT = 4096;            // tokens of a part that PAGES covers at pages of 16 (plus one page of offset)
 
@@ -843,7 +890,11 @@ hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
     launch_many<BF16, D, 8, SINKS>(a, rows, st);
   if (a.splits > 1) {
     const int64_t total = a.t.tokens * a.q_heads, nx = std::min<int64_t>(total, 1 << 22);   // nx * 256 threads fit 32 bits
-    attend_join_kernel<BF16, D><<<dim3((unsigned)nx, (unsigned)((total + nx - 1) / nx)), 256, 0, st>>>(a);
+    constexpr int NG = 1024 / D;
+    if (a.splits <= std::min(NG, 8) && total >= JOIN_ROWS && total / NG < 1 << 22)
+      attend_join_rows_kernel<BF16, D><<<(unsigned)((total + NG - 1) / NG), 256, 0, st>>>(a);
+    else
+      attend_join_kernel<BF16, D><<<dim3((unsigned)nx, (unsigned)((total + nx - 1) / nx)), 256, 0, st>>>(a);
   }
   return hipGetLastError();
 }
@@ -862,9 +913,52 @@ hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
 // from Python; 8 of 2000: 13.2 in parts, 16.2 whole). But at least enough
 // parts of 1024 tokens to fill the GPU, since lengths are ragged.
 // Many rows: parts until the row tiles fill the GPU twice.
-AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
-                        int D, int num_cu) {
+// Many rows with a window and first tokens: row tiles are of equal length, that of
+// the window and of the tile's own tokens, so whole rounds of workgroups decide.
+// The shape and the number of parts that a time estimate likes best, for heads of
+// 128: 10 us a workgroup and, a step of 64 tokens, 2.2 us for 128 rows alone on a
+// CU, 3.0 beside another one, 2.4 for 256 rows; parts cost 12 us and 0.4 us a
+// thousand rows and part. 32 query heads, 70 first tokens and a window of 2500: 4096
+// queries 214 us (252 with 128 rows), 1024 queries in two parts of 256 rows 88
+// (97 whole), 200 queries 49 (95 whole); a window of 500: 4096 queries 76 (80),
+// 512 30 (34 with 256 rows).
+static AttnPlan window_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
+                            bool causal, int D, int num_cu) {
   const int64_t rows = max_tokens * group;
+  AttnPlan best{};
+  double least = 1e30;
+  for (int W = 4; W <= (D == 128 ? 8 : 4); W += 4) {
+    const int64_t tokens = causal ? std::min<int64_t>(max_tokens, (32 * W + group - 1) / group + 1) : max_tokens;
+    const int64_t span = std::min(max_len, window + tokens + 16 + (sinks + 15) / 16 * 16);
+    const int64_t tiles = batch * heads * ((rows + 32 * W - 1) / (32 * W));
+    for (int n = 1; n <= 8 && (n == 1 || n * 512 <= span); ++n) {
+      const int64_t len = std::max<int64_t>(128, ((span + n - 1) / n + 127) / 128 * 128);
+      const double steps = (double)((len + 63) / 64), scale = D / 128.0;
+      double us = 0.0;
+      if (W == 8) {
+        us = std::ceil((double)(tiles * n) / num_cu) * (10.0 + 2.4 * scale * steps);
+      } else {
+        const int64_t whole = tiles * n / (2 * num_cu), rest = tiles * n % (2 * num_cu);
+        us = whole * (10.0 + 3.0 * scale * steps);
+        if (rest) us += 10.0 + (rest <= num_cu ? 2.2 : 3.0) * scale * steps;
+      }
+      if (n > 1) us += 12.0 + 0.4e-3 * n * scale * batch * rows * heads;
+      if (us < least) {
+        least = us;
+        best.waves = W;
+        best.split_len = (int)std::min<int64_t>(len, (int64_t)1 << 30);
+        best.splits = (int)std::max<int64_t>(1, (span + len - 1) / len);
+      }
+    }
+  }
+  return best;
+}
+
+AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
+                        bool causal, int D, int num_cu) {
+  const int64_t rows = max_tokens * group;
+  if (sinks && rows > FEW_ROWS)
+    return window_plan(batch, heads, group, max_tokens, max_len, window, sinks, causal, D, num_cu);
   AttnPlan p{};
   p.few = rows <= FEW_ROWS;
   int64_t span = max_len;

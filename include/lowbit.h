@@ -627,8 +627,8 @@ int32_t lowbit_attention_sinks(const lowbit_kv_cache* cache, const int32_t* bloc
                                void* workspace, size_t workspace_bytes, void* stream);
 
 size_t lowbit_attention_sinks_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
-                                              int64_t q_heads, int64_t kv_heads, int64_t head_dim, int64_t window,
-                                              int64_t sinks);
+                                              int64_t q_heads, int64_t kv_heads, int64_t head_dim, int32_t causal,
+                                              int64_t window, int64_t sinks);
 
 /* Several independent linears of one shape in one launch: problem z computes
  *

@@ -134,10 +134,10 @@ def test_attention_sinks_refusals(b):
         assert call(cache=_cache(b, **kw)) == getattr(b, "ERR_" + want), kw
     f, g = b.lib().lowbit_attention_workspace_bytes, b.lib().lowbit_attention_sinks_workspace_bytes
     for win in (0, 100, 5000):
-        assert g(1, 1, 1, 100000, 32, 8, 128, win, 0) == f(1, 1, 1, 100000, 32, 8, 128, win)
-    assert g(1, 1, 1, 100000, 32, 8, 128, 0, 50) == f(1, 1, 1, 100000, 32, 8, 128, 0)
-    assert g(1, 1, 1, 100000, 32, 8, 128, 5000, 100000) >= g(1, 1, 1, 100000, 32, 8, 128, 5000, 4) > 0
-    assert g(1, 1, 1, 100000, 32, 8, 128, 5000, -1) == 0
+        assert g(1, 1, 1, 100000, 32, 8, 128, 1, win, 0) == f(1, 1, 1, 100000, 32, 8, 128, win)
+    assert g(1, 1, 1, 100000, 32, 8, 128, 1, 0, 50) == f(1, 1, 1, 100000, 32, 8, 128, 0)
+    assert g(1, 1, 1, 100000, 32, 8, 128, 1, 5000, 100000) >= g(1, 1, 1, 100000, 32, 8, 128, 1, 5000, 4) > 0
+    assert g(1, 1, 1, 100000, 32, 8, 128, 1, 5000, -1) == 0
 
 
 @made_up_addresses

@@ -166,6 +166,24 @@ def test_attention_sinks_long_prompt_in_256_row_tiles(lb):
             assert ((out[i, h].double() - want).abs() <= 2.0 ** -10 * mag + 2.0 ** -25 * peak + half).all(), (i, h)
 
 
+JOIN = [  # lens, new, H, Hq, page, D, dtype, window, sinks: few parts of many rows
+    ([3000 - 17 * i for i in range(60)], [1] * 60, 1, 16, 16, 128, "bf16", 2500, 20),
+    ([900, 4000], [300, 250], 1, 2, 64, 64, "f16", 3000, 50),
+    ([4000, 20], [300, 20], 1, 2, 64, 256, "bf16", 3000, 50),
+    ([3000], [700], 1, 4, 32, 128, "f16", 2000, 50),
+]
+
+
+@pytest.mark.parametrize("case", JOIN, ids=[str(i) for i in range(len(JOIN))])
+def test_attention_sinks_joined_by_rows(lb, case):
+    lens, new, H, Hq, page, D, dt, window, sinks = case
+    banner(f"attention, join by rows: {len(lens)} sequences, heads of {D}")
+    B, T = len(lens), sum(new)
+    need = lb.lib().lowbit_attention_sinks_workspace_bytes(B, T, max(new), max(lens), Hq, H, D, 1, window, sinks)
+    assert 2 <= need // (T * Hq * (D + 2) * 4) <= 8           # parts
+    _attend(lb, lens, new, H, Hq, page, D, dt, window, sinks, seed=77)
+
+
 def test_attention_sinks_leaves_rows_of_no_sequence(lb):
     banner("attention with first tokens, padded batch")
     P = Paged([4000, 500], 1, 16, 64, seed=12)
