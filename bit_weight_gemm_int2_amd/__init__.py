@@ -659,16 +659,16 @@ def _counter(dev: int, bad_count, n: int):
 
 def _norms(dev: int, D: int, q_norm, k_norm) -> int:
     """The type of the norms' weights, checked."""
-    dtype = None
-    for t, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if t is None:
-            continue
+    first = k_norm if q_norm is None else q_norm
+    if first is None:
+        return NONE
+    dtype = first.dtype
+    for t in (first,) if k_norm is None or k_norm is first else (first, k_norm):
         if t.get_device() != dev:
-            raise _same_device(dev, **{name: t})
-        if t.shape != (D,) or t.dtype not in _DT or not t.is_contiguous() or t.dtype != (dtype or t.dtype):
+            raise _same_device(dev, **{"q_norm" if t is q_norm else "k_norm": t})
+        if t.shape != (D,) or t.dtype != dtype or dtype not in _DT or not t.is_contiguous():
             raise ValueError(f"q_norm and k_norm must be contiguous float16, bfloat16 or float32 [{D}] of one type")
-        dtype = t.dtype
-    return NONE if dtype is None else _DT[dtype]
+    return _DT[dtype]
 
 
 def kv_append(k: torch.Tensor, v: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tokens: torch.Tensor,
@@ -896,27 +896,35 @@ def rope_tables(positions: int, rot: int, base: float = 1e4, scaling: Optional[s
     write into."""
     if scaling not in _ROPE:
         raise ValueError(f"scaling must be None, 'linear', 'ntk', 'yarn' or 'wavelength', not {scaling!r}")
-    shape = (positions, rot // 2)
-    if out is None:
-        dev = torch.device("cuda" if device is None else device)
-        if dev.type != "cuda":
-            raise ValueError("the tables must be on a GPU")
-        index = torch._C._cuda_getDevice() if dev.index is None else dev.index
-    else:
+    if out is not None:
         cos, sin = out
         index = cos.get_device()
         if index < 0 or sin.get_device() != index:
             raise _same_device(index, sin=sin)
         for t in out:
-            if t.shape != shape or t.dtype != torch.float32 or not t.is_contiguous():
-                raise ValueError(f"cos and sin must be contiguous float32 {list(shape)}")
-    if torch._C._cuda_getDevice() != index:   # the library launches for the current device
+            if t.shape != (positions, rot // 2) or t.dtype != torch.float32 or not t.is_contiguous():
+                raise ValueError(f"cos and sin must be contiguous float32 {[positions, rot // 2]}")
+    elif device is None:
+        index = None
+    else:
+        dev = torch.device(device)
+        if dev.type != "cuda":
+            raise ValueError("the tables must be on a GPU")
+        index = dev.index
+    current = torch._C._cuda_getDevice()
+    if index is None:
+        index = current
+    elif current != index:                    # the library launches for the current device
         with torch.cuda.device(index):
-            return rope_tables(positions, rot, base, scaling, factor, original, low, high, magnitude, first,
-                               torch.device("cuda", index), out, stream)
+            return rope_tables(positions, rot, base, scaling, factor, original, low, high, magnitude, first, index, out, stream)
     if out is None:
-        with torch.cuda.stream(stream):       # no stream given: the current one
-            cos, sin = (torch.empty(shape, dtype=torch.float32, device=torch.device("cuda", index)) for _ in range(2))
+        if positions < 0 or rot < 0:
+            raise LowbitError(ERR_SHAPE, "lowbit_rope_tables")
+        if stream is None:
+            cos, sin = torch.empty((2, positions, rot // 2), dtype=torch.float32, device=index).unbind(0)
+        else:
+            with torch.cuda.stream(stream):   # memory of the stream that writes it
+                cos, sin = torch.empty((2, positions, rot // 2), dtype=torch.float32, device=index).unbind(0)
     _check(lib().lowbit_rope_tables(cos.data_ptr(), sin.data_ptr(), positions, rot, first, base, _ROPE[scaling], factor,
                                     original, low, high, 0.0 if magnitude is None else magnitude, _queue(stream, index)),
            "lowbit_rope_tables")
@@ -924,10 +932,10 @@ def rope_tables(positions: int, rot: int, base: float = 1e4, scaling: Optional[s
 
 
 class PagePlan(NamedTuple):
-    """What kv_remap returns: the new table and lengths, the pages to copy in
-    every layer's cache (kv_copy_pages(cache, plan.src, plan.dst,
-    plan.counts)), and counts: pairs, pages in use afterwards, slots that found
-    no page, moves among the pairs."""
+    """What kv_remap returns, views of one tensor: the new table and lengths,
+    the pages to copy in every layer's cache (kv_copy_pages(cache, plan.src,
+    plan.dst, plan.counts)), and counts: pairs, pages in use afterwards, slots
+    that found no page, moves among the pairs."""
     table: torch.Tensor
     lens: torch.Tensor
     src: torch.Tensor
@@ -954,14 +962,12 @@ def kv_remap(block_table: torch.Tensor, lens: torch.Tensor, cache: KVCache, rows
     if torch._C._cuda_getDevice() != dev:     # the library plans and launches for the current device
         with torch.cuda.device(dev):
             return kv_remap(block_table, lens, cache, rows, room, window, sinks, compact, width, workspace, stream)
-    named = dict(block_table=block_table, lens=lens)
-    if rows is not None:
-        named["rows"] = rows
-    if room is not None:
-        named["room"] = room
-    for t in named.values():
+    for t in (block_table, lens, rows, room):
+        if t is None:
+            continue
         if t.get_device() != dev:
-            raise _same_device(dev, **named)
+            raise _same_device(dev, **{n: x for n, x in (("block_table", block_table), ("lens", lens), ("rows", rows),
+                                                         ("room", room)) if x is not None})
         if t.dtype != torch.int32 or not t.is_contiguous():
             raise ValueError("block_table, lens, rows and room must be contiguous int32 tensors")
     if block_table.dim() != 2:
@@ -980,20 +986,20 @@ def kv_remap(block_table: torch.Tensor, lens: torch.Tensor, cache: KVCache, rows
     need = L.lowbit_kv_remap_workspace_bytes(n, pages)
     if pairs < 0 or wide < 0 or not need:
         raise LowbitError(ERR_SHAPE, "lowbit_kv_remap")
-    size = need
+    own = 0                                   # the workspace's words in front of the results, where none is given
     if workspace is None:
-        workspace = _new(need, torch.uint8, block_table, stream)
+        own, size = need // 4, need
     else:
         size = _given_workspace(workspace, need, "lowbit_kv_remap")
         if workspace.get_device() != dev:
             raise _same_device(dev, workspace=workspace)
-    made = _new(n * wide + n + 2 * pairs + 4, torch.int32, block_table, stream)
-    table, new_lens, src, dst, counts = made.split((n * wide, n, pairs, pairs, 4))
+    made = _new(own + n * wide + n + 2 * pairs + 4, torch.int32, block_table, stream)
+    at, table, new_lens, src, dst, counts = made.split_with_sizes((own, n * wide, n, pairs, pairs, 4))
     plan = PagePlan(table.view(n, wide), new_lens, src, dst, counts)
     _check(L.lowbit_kv_remap(block_table.data_ptr(), old, lens.data_ptr(), batch, pages, cache.page, _ptr(rows), _ptr(room), n,
                              window, sinks, compact, table.data_ptr(), wide, new_lens.data_ptr(), src.data_ptr(),
-                             dst.data_ptr(), pairs, counts.data_ptr(), workspace.data_ptr(), size, _queue(stream, dev)),
-           "lowbit_kv_remap")
+                             dst.data_ptr(), pairs, counts.data_ptr(), (workspace if at.numel() == 0 else at).data_ptr(), size,
+                             _queue(stream, dev)), "lowbit_kv_remap")
     return plan
 
 
