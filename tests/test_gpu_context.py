@@ -687,3 +687,24 @@ def test_together_in_a_graph(lb):
         assert all(torch.equal(a, b) for a, b in zip(res, eager))
         put_back()
         assert all(torch.equal(a, b) for a, b in zip(step(), eager))
+
+
+@pytest.mark.parametrize("flags", [["--window", "16", "--sinks", "3", "--answers", "3", "--head-norms", "--scaling", "yarn"],
+                                   ["--answers", "2", "--scaling", "wavelength", "--tokens", "1"],
+                                   ["--head-norms", "--scaling", "ntk", "--window", "5"]])
+def test_example_with_windows_norms_and_answers(lb, capsys, monkeypatch, flags):
+    """The example program on a small model against float64: 2 % a layer, as in
+    test_gpu_decode.py (the norm of a head adds one rounding, of the weights none)."""
+    banner(f"example: {flags}")
+    import importlib.util
+    import os
+    import sys
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "text_decode.py")
+    spec = importlib.util.spec_from_file_location("text_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    monkeypatch.setattr(sys, "argv", ["text_decode", "--layers", "2", "--hidden", "256", "--q-heads", "6", "--kv-heads", "2",
+                                      "--head-dim", "64", "--mlp", "384", "--vocab", "500", "--page", "16", "--batch", "2",
+                                      "--prompt", "37", "--tokens", "9", "--check", *flags])
+    m.main()
+    assert "relative difference" in capsys.readouterr().out
