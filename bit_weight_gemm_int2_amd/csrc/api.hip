@@ -728,7 +728,7 @@ int32_t kv_append(const lowbit_kv_cache* cache, const int32_t* block_table, int6
   if (rot < 0 || rot > D || rot % 32 || (rot && (rope_rows < 1 || rope_rows >= kMaxDim))) return LOWBIT_ERR_SHAPE;
   if ((rot != 0) != (cos != nullptr) || (rot != 0) != (sin != nullptr)) return LOWBIT_ERR_NULL;
   if ((q == nullptr) != (q_out == nullptr)) return LOWBIT_ERR_NULL;
-  if ((st = check_norms(norms, q != nullptr))) return st;
+  if ((st = check_norms(norms, q || !tokens))) return st;   // no tokens: an empty array may have no address
   if (q && (q_heads < 1 || q_heads > 65536)) return LOWBIT_ERR_SHAPE;
   if (!aligned(cos, 16) || !aligned(sin, 16) || !aligned(bad_count, 4)) return LOWBIT_ERR_ALIGN;
   if (!tokens) return LOWBIT_OK;
@@ -1048,7 +1048,7 @@ int32_t lowbit_rope_tables(float* cos, float* sin, int64_t positions, int64_t ro
     if (scaling == LOWBIT_ROPE_WAVELENGTH)
       less = 1.0 - std::min(std::max((original * f / turn - low) / (high - low), 0.0), 1.0);
     if (less > 0.0) f = f * (1.0 - less) + f / factor * less;
-    g.quarters[i] = f / turn * 4.0;
+    g.turns[i] = (uint64_t)std::llround(std::ldexp(f / 6.283185307179586476925286766559L, 64));
   }
   g.magnitude = magnitude > 0.0                 ? (float)magnitude
                 : scaling == LOWBIT_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0)
@@ -1138,7 +1138,7 @@ int32_t lowbit_kv_remap(const int32_t* block_table, int64_t table_width, const i
   g.compact = compact != 0;
   g.most = (int)std::min<int64_t>(std::min(table_width, new_width) * page, 0x7fffffff);
   g.window = std::min<int64_t>(window, kMaxDim);            // larger ones hold every token
-  g.sinks = sinks;
+  g.sinks = std::min<int64_t>(sinks, kMaxDim);
   g.table_out = new_table;
   g.lens_out = new_lens;
   g.src = src;

@@ -100,7 +100,7 @@ struct TableArgs {
   int64_t n, first;
   int half;
   float magnitude;
-  double quarters[kMaxPairs];       // a position's angle in quarter turns, at most 2 / pi
+  uint64_t turns[kMaxPairs];        // a position's angle in turns of 2^64
 };
 
 struct AttnArgs {

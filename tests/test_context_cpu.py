@@ -93,12 +93,12 @@ def test_remap_by_hand():
 @made_up_addresses
 def test_kv_append_norm_refusals(b):
     Q = P + (8 << 32)
-    good = dict(q=Q + 2048, qo=P + (9 << 32), qn=P + (12 << 32), kn=P + (13 << 32), nd=b.BF16, eps=1e-6, bad=None)
+    good = dict(q=Q + 2048, qo=P + (9 << 32), qn=P + (12 << 32), kn=P + (13 << 32), nd=b.BF16, eps=1e-6, bad=None, T=40)
 
     def call(**kw):
         a = dict(good, **kw)
         return b.lib().lowbit_kv_append_norm(
-            _cache(b), P + (4 << 32), 10, P + (5 << 32), P + (6 << 32), 3, 40, 20, b.BF16, Q, 1536, 128, Q + 1024, 1536, 128,
+            _cache(b), P + (4 << 32), 10, P + (5 << 32), P + (6 << 32), 3, a["T"], 20, b.BF16, Q, 1536, 128, Q + 1024, 1536, 128,
             a["q"], 1536, 128, 4, a["qo"], 512, 128, P + (10 << 32), P + (11 << 32), 128, 500, 0, a["qn"], a["kn"], a["nd"],
             a["eps"], a["bad"], None)
 
@@ -106,6 +106,7 @@ def test_kv_append_norm_refusals(b):
     assert call(qn=None) == b.ERR_DEVICE and call(kn=None) == b.ERR_DEVICE and call(eps=0.0) == b.ERR_DEVICE
     assert call(qn=None, kn=None, nd=b.NONE) == b.ERR_DEVICE
     assert call(qn=None, q=None, qo=None) == b.ERR_DEVICE
+    assert call(T=0, q=None, qo=None) == b.OK                 # no tokens: empty arrays may have no address
     for kw, want in ((dict(q=None, qo=None), "NULL"), (dict(qn=None, kn=None), "NULL"), (dict(nd=b.NONE), "DTYPE"),
                      (dict(nd=17), "DTYPE"), (dict(eps=-1.0), "SHAPE"), (dict(eps=float("nan")), "SHAPE"),
                      (dict(eps=float("inf")), "SHAPE"), (dict(kn=P + 8 + (13 << 32)), "ALIGN"),

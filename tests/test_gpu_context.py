@@ -305,6 +305,36 @@ def test_rows_of_many_tokens_and_heads(lb):
         assert ((y.double() - z).abs() <= z.abs() * 1.01 * 2.0 ** -8 + 2.0 ** -19).all()
 
 
+def test_calls_without_tokens(lb):
+    banner("append with norms, norm and rotation, attention: no tokens")
+    x, w = torch.empty((0, 2, 64), device="cuda").half(), torch.ones(64, device="cuda").half()
+    cache = lb.new_kv_cache(2, 2, 16, 64)
+    cos, sin = lb.rope_tables(10, 64)
+    for batch in (0, 3):
+        where = (_i32(np.zeros((batch, 1))), _i32(np.zeros(batch + 1)), _i32(np.zeros(batch)))
+        q = lb.kv_append(x, x, cache, *where, 1, q=x, cos=cos, sin=sin, q_norm=w, k_norm=w)
+        assert q.shape == x.shape
+        assert lb.attention(q, cache, *where, 1, 10, window=5, sinks=2).shape == x.shape
+    q, k = lb.norm_rotate(x, x, w, w, cos, sin)
+    assert q.shape == k.shape == x.shape
+
+
+def test_norm_rotate_in_more_than_one_launch(lb):
+    """More units than one launch takes: 8200 tokens of 65536 heads."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 120 << 30:
+        pytest.skip("needs 120 GiB of free GPU memory")
+    banner("norm and rotation: 8200 tokens of 65536 heads")
+    x = torch.randn((1, 65536, 64), device="cuda").half().expand(8200, -1, -1)     # one token's rows, read again for each
+    w = torch.ones(64, device="cuda").half()
+    cos, sin = lb.rope_tables(8200, 64)
+    y = lb.norm_rotate(x, q_norm=w, cos=cos, sin=sin)
+    at = [0, 1, 8190, 8191, 8192, 8193, 8199]
+    assert torch.equal(y[at], lb.norm_rotate(x[at], q_norm=w, cos=cos, sin=sin, positions=_i32(at)))
+    del y
+    torch.cuda.empty_cache()
+
+
 APPEND = [  # starts, new, H, Hq, page, D, rot, interleaved, dtype, weights' dtype
     ([0], [1], 1, 1, 16, 64, 64, False, "bf16", "bf16"),
     ([15, 16, 17], [1, 1, 1], 2, 6, 16, 64, 32, True, "f16", "f32"),
