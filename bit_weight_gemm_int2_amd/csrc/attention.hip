@@ -98,11 +98,12 @@ __device__ __forceinline__ float sum16(float x) { return sum32(x + __shfl_xor(x,
 // What one row tile has to do: rows [row0, row0 + rows) of (token, head in
 // group) pairs of one sequence and key/value head, tokens [t0, t1) of its
 // context.
-// (SINKS: a place u of the tile's context is token u before `head`, token u + skip from there on; t0 and t1 are places,
-// t1 .. end the last one's token. Else places are tokens.)
+// (SINKS: in places. Place u of the tile's context is token u before `head`, token u + skip from there on. A window that
+// begins behind the head is one of places too, less `skip`, and places before the head are tokens: masks go by places,
+// pages by tokens.)
 struct Work {
   int64_t lo;                              // first row of the sequence in the dense operands
-  int n, rows, row0, len, t0, t1, end, head, skip;
+  int n, rows, row0, len, t0, t1, head, skip;
   __device__ __forceinline__ int pos(int row, int group) const { return len - n + row / group; }
   template <bool SINKS> __device__ __forceinline__ int token(int u) const { return SINKS && u >= head ? u + skip : u; }
 };
@@ -133,7 +134,6 @@ __device__ __forceinline__ bool find_work(const AttnArgs& a, int b, int row0, in
   w->t1 = (int)min((int64_t)end, beg + ((int64_t)split + 1) * a.split_len);
   // a part behind the last token holds no place (with SINKS no token before t0 is masked, so none may be read)
   if (SINKS && w->t0 == w->t1) w->t0 = w->t1 = w->t1 & ~15;
-  w->end = SINKS && w->t1 > w->head ? w->t1 + w->skip : w->t1;
   return true;
 }
 
@@ -324,21 +324,10 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
           for (int e = 0; e < 4; ++e) qf[i][k][e] = pack2(x[i][k][2 * e] * by, x[i][k][2 * e + 1] * by);
     }
     const int pos = w.pos(w.row0 + min(r, w.rows - 1), a.group);
-    const int hi = a.causal ? min(w.end, pos + 1) : w.end, lo = a.window ? pos - a.window + 1 : 0;
+    const int hi = a.causal ? min(w.t1, pos + 1 - w.skip) : w.t1, lo = a.window ? pos - a.window + 1 - w.skip : 0;
     // tokens that no row of the tile masks
-    const int pos0 = w.pos(w.row0, a.group), pos1 = w.pos(w.row0 + w.rows - 1, a.group);
-    const int all_hi = a.causal ? min(w.end, pos0 + 1) : w.end, all_lo = a.window ? pos1 - a.window + 1 : 0;
-    // whether some row masks a token of the step at place t
-    auto masked = [&](int t) __attribute__((always_inline)) {
-      if constexpr (!SINKS) return t < all_lo || t < w.t0 || t + 32 > all_hi;
-      bool some = false;
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int tok = w.token<SINKS>(t + 16 * j);
-        some |= tok + 16 > all_hi || (tok < all_lo && tok + 16 > a.sinks);
-      }
-      return some;
-    };
+    const int pos0 = w.pos(w.row0, a.group) - w.skip, pos1 = w.pos(w.row0 + w.rows - 1, a.group) - w.skip;
+    const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = a.window ? pos1 - a.window + 1 : 0;
     __syncthreads();
 
     for (; t < w.t1; t += STEP) {
@@ -368,13 +357,13 @@ __global__ __launch_bounds__(256) void attend_few_kernel(AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) s[j][e] = __builtin_fmaf(s[j][e], kf, lv);
       }
-      if (masked(t)) {
+      if (t < all_lo || t < w.t0 || t + 32 > all_hi) {
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int tok = w.token<SINKS>(t + 16 * j) + 4 * g + e;
-            if ((tok < lo && !(SINKS && tok < a.sinks)) || (!SINKS && tok < w.t0) || tok >= hi) s[j][e] = NEG_INF;
+            const int tok = t + 16 * j + 4 * g + e;
+            if ((tok < lo && !(SINKS && tok < a.sinks)) || tok < w.t0 || tok >= hi) s[j][e] = NEG_INF;
           }
       }
 #pragma unroll
@@ -539,36 +528,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
     }
   };
   const int pos = w.pos(w.row0 + rr, a.group);
-  const int first = SINKS ? 0 : w.t0;                                  // no token before it is read
-  const int hi = a.causal ? min(w.end, pos + 1) : w.end, lo = max(first, a.window ? pos - a.window + 1 : 0);
+  const int hi = a.causal ? min(w.t1, pos + 1 - w.skip) : w.t1, lo = max(w.t0, a.window ? pos - a.window + 1 - w.skip : 0);
   // tokens that no row of this wave masks
   const int f0 = min(32 * wave, w.rows - 1), f1 = min(32 * wave + 31, w.rows - 1);
-  const int pos0 = w.pos(w.row0 + f0, a.group), pos1 = w.pos(w.row0 + f1, a.group);
-  const int all_hi = a.causal ? min(w.end, pos0 + 1) : w.end, all_lo = max(first, a.window ? pos1 - a.window + 1 : 0);
+  const int pos0 = w.pos(w.row0 + f0, a.group) - w.skip, pos1 = w.pos(w.row0 + f1, a.group) - w.skip;
+  const int all_hi = a.causal ? min(w.t1, pos0 + 1) : w.t1, all_lo = max(w.t0, a.window ? pos1 - a.window + 1 : 0);
   // tokens that some row of this wave sees
-  const int any_hi = 32 * wave >= w.rows ? 0 : a.causal ? min(w.end, pos1 + 1) : w.end;
-  const int any_lo = max(first, a.window ? pos0 - a.window + 1 : 0);
-  // whether no row of this wave sees a token of the tile at place t, and whether some row masks one
-  auto unseen = [&](int t) __attribute__((always_inline)) {
-    if constexpr (!SINKS) return t >= any_hi || t + TOK <= any_lo;
-    bool all = true;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int tok = w.token<SINKS>(t + 16 * u);
-      all &= tok >= any_hi || (tok + 16 <= any_lo && tok >= a.sinks);
-    }
-    return all;
-  };
-  auto masked = [&](int t) __attribute__((always_inline)) {
-    if constexpr (!SINKS) return t < all_lo || t + TOK > all_hi;
-    bool some = false;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int tok = w.token<SINKS>(t + 16 * u);
-      some |= tok + 16 > all_hi || (tok < all_lo && tok + 16 > a.sinks);
-    }
-    return some;
-  };
+  const int any_hi = 32 * wave >= w.rows ? 0 : a.causal ? min(w.t1, pos1 + 1) : w.t1, any_lo = max(w.t0, a.window ? pos0 - a.window + 1 : 0);
+  const int seen = w.head ? w.head : a.sinks;                          // with first tokens, none of them is there or behind
 
   float m = NEG_INF, l = 0.0f;
   f32x16 o[D / 32];
@@ -650,7 +617,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
       const uint8_t* ks = smem + buf * many::stage<D>();
       const uint8_t* vs = ks + KB;
       uint8_t* const to = smem + (buf ^ 1) * many::stage<D>();
-      if (unseen(t)) {
+      // (as one truth value from all of it, the same test costs 26 registers and spills)
+      if (t >= any_hi || (t + TOK <= any_lo && (!SINKS || t >= seen))) {
         stage(to);
         fetch(t + 2 * TOK);
       } else {
@@ -677,12 +645,12 @@ __global__ __launch_bounds__(64 * W, D == 256 ? W / 4 : 2) void attend_many_kern
 #pragma unroll
           for (int e = 8 * (u & 1); e < 8 * (u & 1) + 8; ++e) s[u >> 1][e] = __builtin_fmaf(s[u >> 1][e], kf, lv);
         }
-        if (masked(t)) {
+        if (t < all_lo || t + TOK > all_hi) {
 #pragma unroll
           for (int j = 0; j < 2; ++j)
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const int tok = w.token<SINKS>(t + 32 * j + 16 * (e >> 3)) + (e & 3) + 8 * (e >> 2 & 1) + 4 * hh;
+              const int tok = t + 32 * j + (e & 3) + 8 * (e >> 2) + 4 * hh;
               if ((tok < lo && !(SINKS && tok < a.sinks)) || tok >= hi) s[j][e] = NEG_INF;
             }
         }
@@ -915,34 +883,38 @@ hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
 // Many rows: parts until the row tiles fill the GPU twice.
 // Many rows with a window and first tokens: row tiles are of equal length, that of
 // the window and of the tile's own tokens, so whole rounds of workgroups decide.
-// The shape and the number of parts that a time estimate likes best, for heads of
-// 128: 10 us a workgroup and, a step of 64 tokens, 2.2 us for 128 rows alone on a
-// CU, 3.0 beside another one, 2.4 for 256 rows; parts cost 12 us and 0.4 us a
-// thousand rows and part. 32 query heads, 70 first tokens and a window of 2500: 4096
-// queries 214 us (252 with 128 rows), 1024 queries in two parts of 256 rows 88
-// (97 whole), 200 queries 49 (95 whole); a window of 500: 4096 queries 76 (80),
-// 512 30 (34 with 256 rows).
+// The shape and the number of parts that a time estimate likes best: `fixed` us a
+// workgroup and, a step of 64 tokens, `step` us with one, two or three workgroups a
+// CU; parts cost 6 us and, a thousand rows, 0.2 and 0.25 a part. 32 query heads of
+// 128, 70 first tokens and a window of 2500: 4096 queries 193 us in tiles of 256
+// rows (209 of 128), 3000 queries 162 of 128 (178 of 256), 1024 queries 69 (83 in two
+// parts), 512 queries 59 in four parts (68 whole), 64 queries 31 in eight (67 whole).
 static AttnPlan window_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
                             bool causal, int D, int num_cu) {
+  struct Shape {
+    int D, waves, most;                    // workgroups of a CU
+    double fixed, step[3];
+  };
+  static const Shape shapes[] = {{64, 4, 3, 9.0, {0.95, 1.44, 2.01}},
+                                 {128, 4, 2, 9.0, {1.41, 2.33, 0.0}},
+                                 {128, 8, 1, 11.0, {2.07, 0.0, 0.0}},
+                                 {256, 4, 1, 20.0, {2.92, 0.0, 0.0}}};
   const int64_t rows = max_tokens * group;
   AttnPlan best{};
   double least = 1e30;
-  for (int W = 4; W <= (D == 128 ? 8 : 4); W += 4) {
+  for (const Shape& s : shapes) {
+    if (s.D != D) continue;
+    const int W = s.waves;
     const int64_t tokens = causal ? std::min<int64_t>(max_tokens, (32 * W + group - 1) / group + 1) : max_tokens;
     const int64_t span = std::min(max_len, window + tokens + 16 + (sinks + 15) / 16 * 16);
     const int64_t tiles = batch * heads * ((rows + 32 * W - 1) / (32 * W));
     for (int n = 1; n <= 8 && (n == 1 || n * 512 <= span); ++n) {
       const int64_t len = std::max<int64_t>(128, ((span + n - 1) / n + 127) / 128 * 128);
-      const double steps = (double)((len + 63) / 64), scale = D / 128.0;
-      double us = 0.0;
-      if (W == 8) {
-        us = std::ceil((double)(tiles * n) / num_cu) * (10.0 + 2.4 * scale * steps);
-      } else {
-        const int64_t whole = tiles * n / (2 * num_cu), rest = tiles * n % (2 * num_cu);
-        us = whole * (10.0 + 3.0 * scale * steps);
-        if (rest) us += 10.0 + (rest <= num_cu ? 2.2 : 3.0) * scale * steps;
-      }
-      if (n > 1) us += 12.0 + 0.4e-3 * n * scale * batch * rows * heads;
+      const double steps = (double)((len + 63) / 64);
+      const int64_t round = (int64_t)s.most * num_cu, rest = tiles * n % round;
+      double us = tiles * n / round * (s.fixed + s.step[s.most - 1] * steps);
+      if (rest) us += s.fixed + s.step[(rest - 1) / num_cu] * steps;
+      if (n > 1) us += 6.0 + 1e-3 * (0.2 + 0.25 * n + (n > 1024 / D ? 1.6 : 0.0)) * D / 128 * batch * rows * heads;
       if (us < least) {
         least = us;
         best.waves = W;
