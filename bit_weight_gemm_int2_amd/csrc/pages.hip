@@ -359,6 +359,7 @@ __global__ __launch_bounds__(SCAN_THREADS) void remap_kernel(RemapArgs g, int lo
     if (i < words) set.before[i] = run.x + at.x;
     run.x += total.x;
   }
+  __syncthreads();                                           // without rows no other one follows before the counts are read
   const int used = run.x;
   run = {0, 0};
   for (int b = 0; b < R; b += SCAN_THREADS) {

@@ -589,10 +589,47 @@ def test_kv_remap_of_large_tables(lb, compact):
 def test_kv_remap_of_nothing(lb):
     banner("remap: no old sequences, no new ones, tables without a slot")
     _remap_check(lb, np.zeros((0, 4)), np.zeros(0), 10, 16, rows=np.array([-1, 0, 5]), room=np.array([17, 0, 33]))
-    _remap_check(lb, np.array([[3, 1]]), [20], 10, 16, rows=np.zeros(0, dtype=int))
+    for compact in (False, True):
+        for pages in (10, 3000, 100000):                          # all sequences end
+            _remap_check(lb, np.array([[3, 1]]), [20], pages, 16, rows=np.zeros(0, dtype=int), compact=compact)
     _remap_check(lb, np.array([[3, 1]]), [20], 10, 16, rows=np.array([0]), width=0, room=np.array([5]))
     _remap_check(lb, np.zeros((2, 0)), [7, 0], 10, 16, room=np.array([5, 5]), width=2)
     _remap_check(lb, np.array([[0]]), [16], 1, 16, rows=np.array([0, 0]), room=np.array([1, 1]), width=2)   # no page left
+
+
+def test_kv_remap_from_several_threads_and_streams(lb):
+    """Four host threads with streams of their own, each with its own tables; every result as alone."""
+    banner("remap from four threads")
+    import threading
+    g = np.random.default_rng(80)
+    jobs, got, errors = [], [None] * 4, []
+    for i in range(4):
+        table, lens = _random_tables(g, 20 + 90 * i, 30, 30000, 16, 5, 0.01)
+        rows, room = g.integers(-1, len(lens), 50), g.integers(0, 40, 50)
+        jobs.append((table, lens, rows, room, bool(i % 2)))
+    pool = Pool(lb, 30000, 16, 1)
+    args = [(_i32(t), _i32(n), pool.cache, _i32(r), _i32(m)) for t, n, r, m, _ in jobs]
+    torch.cuda.synchronize()
+
+    def work(i):
+        try:
+            s = torch.cuda.Stream()
+            for _ in range(20):
+                got[i] = lb.kv_remap(*args[i], window=100, sinks=20, compact=jobs[i][4], stream=s)
+            s.synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
+    for (table, lens, rows, room, compact), plan in zip(jobs, got):
+        want, L, pairs, counts = od.remap(table, lens, 30000, 16, rows=rows, room=room, window=100, sinks=20, compact=compact)
+        assert plan.counts.tolist() == counts and np.array_equal(plan.table.cpu().numpy(), want)
+        assert list(zip(plan.src.tolist(), plan.dst.tolist()))[:len(pairs)] == pairs and plan.lens.tolist() == L.tolist()
 
 
 def test_kv_copy_pages_lists(lb):
