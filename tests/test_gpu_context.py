@@ -131,14 +131,18 @@ def test_attention_sinks_leaves_the_gap_alone(lb, new):
 @pytest.mark.parametrize("new", [1, 50])
 def test_attention_sinks_beside_the_plain_calls(lb, new):
     """No first tokens, or no window: the same bits as without them; a first
-    token alone beside a window that holds the rest: those of no window."""
+    token alone beside a window that holds the rest: the tokens of no window, in
+    parts of its own (each result is within its bound of the definition)."""
     banner(f"attention: sinks 0, window 0, new {new}")
     P = Paged([700, 30], 2, 32, 128, seed=8)
-    q, _ = _values(np.random.default_rng(9), (new + 1, 8, 128), "bf16")
+    q, hq = _values(np.random.default_rng(9), (new + 1, 8, 128), "bf16")
     args = (q, P.cache(lb), _i32(P.table), _i32([0, new, new + 1]), _i32([700, 30]), new, 700)
     assert torch.equal(lb.attention(*args, window=100, sinks=0), lb.attention(*args, window=100))
     assert torch.equal(lb.attention(*args, window=0, sinks=9), lb.attention(*args))
-    assert torch.equal(lb.attention(*args, window=699, sinks=1), lb.attention(*args))
+    for kw in (dict(window=699, sinks=1), dict()):
+        out, lse = lb.attention(*args, **kw, return_lse=True)
+        _check_attention(P, P.table, hq, to_host64(out), to_host64(lse), [700, 30], [new, 1], [0, new, new + 1], 128, out.dtype,
+                         True, 0, 0)
 
 
 def test_attention_sinks_long_prompt_in_256_row_tiles(lb):
