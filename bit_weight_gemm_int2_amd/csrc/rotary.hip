@@ -107,7 +107,7 @@ __global__ __launch_bounds__(256) void turn_kernel(TurnArgs g) {
   }
   if constexpr (W != DT_NONE) {
     const bool norm = key ? g.w[1] != nullptr : g.w[0] != nullptr;
-    const float by = norm_factor(r, U, 1.0 / g.D, g.eps);
+    const float by = norm_factor(r, norm, U, 1.0 / g.D, g.eps);
 #pragma unroll
     for (int e = 0; e < 16; ++e) r[e] = norm ? r[e] * by * w[e] : r[e];
   }

@@ -113,8 +113,11 @@ __device__ __forceinline__ double other_lane(double x) {
 // consecutive lanes, all active). The squares and their sum are FP64: no FP32
 // value overflows or vanishes there (squares of BF16 values of 2^64 pass FP32's
 // range), and it took no longer than FP32 (28.5 us for 4608 tokens of 48 heads
-// both ways). With a sum of 0 and no eps the row stays 0.
-__device__ __forceinline__ float norm_factor(const float* r, int U, double inv_d, double eps) {
+// both ways). With a sum of 0 and no eps the row stays 0. Without eps the factor
+// of a row of subnormal values passes FP32's range (2^149 of 2^-149): a row whose
+// mean is below 2^-252 is moved up by 2^64 first, to at most 2^-58 (where `norm`:
+// a row that takes none stays as it is).
+__device__ __forceinline__ float norm_factor(float* r, bool norm, int U, double inv_d, double eps) {
   double sum = 0.0;
 #pragma unroll
   for (int e = 0; e < 16; ++e) sum = __builtin_fma((double)r[e], (double)r[e], sum);
@@ -123,10 +126,16 @@ __device__ __forceinline__ float norm_factor(const float* r, int U, double inv_d
   if (U > 4) sum += other_lane<0x141>(sum);                  // the mirrored lane of eight, whose four hold the other sum
   if (U > 8) sum += other_lane<0x140>(sum);                  // and of sixteen
   const double mean = __builtin_fma(sum, inv_d, eps);
-  return mean > 0.0 ? (float)rsqrt(mean) : mean == 0.0 ? 0.0f : __builtin_nanf("");
+  double root = rsqrt(mean);
+  if (norm && mean < 0x1p-252) {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) r[e] *= 0x1p64f;
+    root *= 0x1p-64;
+  }
+  return mean > 0.0 ? (float)root : mean == 0.0 ? 0.0f : __builtin_nanf("");
 }
 __device__ __forceinline__ void norm_unit(float* r, const float* w, int U, double inv_d, double eps) {
-  const float by = norm_factor(r, U, inv_d, eps);
+  const float by = norm_factor(r, true, U, inv_d, eps);
 #pragma unroll
   for (int e = 0; e < 16; ++e) r[e] = r[e] * by * w[e];
 }

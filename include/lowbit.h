@@ -423,8 +423,10 @@ int32_t lowbit_kv_append(const lowbit_kv_cache* cache, const int32_t* block_tabl
  * with the weights w of its operand, then its rotation, scale and codes as
  * above. The squares and their sum are FP64, the rest FP32 (one rounding to
  * `dtype` for the queries, as above): within 2^-21 of the row's largest
- * normalised value (times the largest |(cos, sin)|, 1 in plain tables) before that. A row that holds a NaN becomes NaN, one with an infinity NaN
- * there and 0 elsewhere; a row of zeros with eps = 0 stays zeros.
+ * normalised value (times the largest |(cos, sin)|, 1 in plain tables) before
+ * that, for subnormal rows with eps = 0 too. A row that holds a NaN becomes NaN,
+ * one with an infinity NaN there and 0 elsewhere; a row of zeros with eps = 0
+ * stays zeros.
  *   q_norm, k_norm  [head_dim] of norm_dtype (F16, BF16, F32), 16-byte aligned;
  *                   each nullable: no norm of that operand (both NULL with
  *                   norm_dtype NONE: lowbit_kv_append). q_norm needs q.

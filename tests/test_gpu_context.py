@@ -297,6 +297,35 @@ def test_norm_of_huge_tiny_zero_and_nonfinite_rows(lb):
     assert np.allclose(y, h[2] * 2 / np.sqrt(np.float64(np.float32(1e-6))), rtol=2.0 ** -21, atol=0)
 
 
+@pytest.mark.parametrize("dt", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+def test_norm_of_subnormal_rows(lb, dt):
+    """Rows whose root mean square has no FP32 inverse: without eps they have a norm like any others."""
+    banner(f"norm of subnormal rows {dt}")
+    g = np.random.default_rng(11)
+    h = g.standard_normal((6, 1, 128)) * 2.0 ** -126
+    h[1] *= 2.0 ** -6
+    h[2] *= 2.0 ** -120                                          # all 0 but where it is moved up below
+    h[2, 0, 5], h[2, 0, 77] = 2.0 ** -133, -2.0 ** -132          # BF16's smallest value, and twice that
+    h[3] *= 2.0 ** 20                                            # a mean just above 2^-252 x 2^40
+    h[4] *= 2.0 ** 1                                             # a mean around 2^-250
+    x = torch.from_numpy(h).to(dt).cuda()
+    h = to_host64(x)
+    w = torch.full((128,), 2.0, device="cuda")
+    got, same = lb.norm_rotate(x, x, q_norm=w, eps=0.0)
+    want = od.norm(h, 2.0, 0.0)
+    big = np.abs(want).max(-1, keepdims=True)
+    assert (big[[0, 1, 2, 3, 4]] > 1).all()
+    assert (np.abs(to_host64(got) - want) <= 2.0 ** -21 * big + 1.001 * _half_ulp(want, got.dtype)).all()
+    assert torch.equal(same, x)                                  # keys without a norm stay as they are
+    # and in the append: the same norm, then the same codes
+    a, b = (lb.new_kv_cache(1, 1, 16, 128) for _ in range(2))
+    where = (_i32([[0]]), _i32([0, 6]), _i32([0]), 6)
+    lb.kv_append(x, x, a, *where, k_norm=w, eps=0.0)
+    y = lb.norm_rotate(x.float(), q_norm=w, eps=0.0)
+    lb.kv_append(y, x.float(), b, *where)
+    assert torch.equal(a.k, b.k) and torch.equal(a.k_scale, b.k_scale)
+
+
 def test_rows_of_many_tokens_and_heads(lb):
     """The most heads that a call takes, and one head of many tokens."""
     banner("norm of 65536 heads, and of 300000 tokens")
