@@ -1040,15 +1040,19 @@ int32_t lowbit_rope_tables(float* cos, float* sin, int64_t positions, int64_t ro
   auto dimension = [&](double turns) { return rot * std::log(original / (turn * turns)) / (2 * std::log(base)); };
   const double from = bands ? std::max(std::floor(dimension(high)), 0.0) : 0.0;
   const double to = bands ? std::min(std::ceil(dimension(low)), (double)rot - 1) : 0.0;
+  // Powers of two, and plain products for the turns: the loop is a part of each call (16 positions into given tables of
+  // rot 256, from Python: 7.9 us with pow, long double and llround, 5.2). A frequency 2^-x is off by x 2^-x 2^-52, the
+  // turns by 2^-52 of theirs.
+  const double powers = 2.0 * std::log2(base) / rot, turns = 18446744073709551616.0 / turn;
   for (int i = 0; i < g.half; ++i) {
-    double f = std::pow(base, -2.0 * i / rot);
+    double f = i ? std::exp2(-powers * i) : 1.0;             // a base beyond FP64's range has powers of 0
     double less = 0.0;                                       // share of the frequency that is divided by the factor
     if (scaling == LOWBIT_ROPE_LINEAR) less = 1.0;
     if (scaling == LOWBIT_ROPE_YARN) less = std::min(std::max((i - from) / std::max(to - from, 1e-3), 0.0), 1.0);
     if (scaling == LOWBIT_ROPE_WAVELENGTH)
       less = 1.0 - std::min(std::max((original * f / turn - low) / (high - low), 0.0), 1.0);
     if (less > 0.0) f = f * (1.0 - less) + f / factor * less;
-    g.turns[i] = (uint64_t)std::llround(std::ldexp(f / 6.283185307179586476925286766559L, 64));
+    g.turns[i] = (uint64_t)(f * turns + 0.5);
   }
   g.magnitude = magnitude > 0.0                 ? (float)magnitude
                 : scaling == LOWBIT_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0)
