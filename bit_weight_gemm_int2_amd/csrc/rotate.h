@@ -113,10 +113,11 @@ __device__ __forceinline__ double other_lane(double x) {
 // consecutive lanes, all active). The squares and their sum are FP64: no FP32
 // value overflows or vanishes there (squares of BF16 values of 2^64 pass FP32's
 // range), and it took no longer than FP32 (28.5 us for 4608 tokens of 48 heads
-// both ways). With a sum of 0 and no eps the row stays 0. Without eps the factor
-// of a row of subnormal values passes FP32's range (2^149 of 2^-149): a row whose
-// mean is below 2^-252 is moved up by 2^64 first, to at most 2^-58 (where `norm`:
-// a row that takes none stays as it is).
+// both ways). With a sum of 0 and no eps the row stays 0. The factor of a row of
+// subnormal values without eps passes FP32's range (2^149 of 2^-149), and that of a
+// row beyond 2^126 is subnormal itself, with 22 bits or fewer: a row whose mean is
+// below 2^-252 or above 2^252 is moved up or down by 2^64 first, so that the factor
+// is a normal number (where `norm`: a row that takes none stays as it is).
 __device__ __forceinline__ float norm_factor(float* r, bool norm, int U, double inv_d, double eps) {
   double sum = 0.0;
 #pragma unroll
@@ -127,10 +128,11 @@ __device__ __forceinline__ float norm_factor(float* r, bool norm, int U, double 
   if (U > 8) sum += other_lane<0x140>(sum);                  // and of sixteen
   const double mean = __builtin_fma(sum, inv_d, eps);
   double root = rsqrt(mean);
-  if (norm && mean < 0x1p-252) {
+  if (norm && (mean < 0x1p-252 || mean > 0x1p252)) {
+    const float by = mean < 1.0 ? 0x1p64f : 0x1p-64f;
 #pragma unroll
-    for (int e = 0; e < 16; ++e) r[e] *= 0x1p64f;
-    root *= 0x1p-64;
+    for (int e = 0; e < 16; ++e) r[e] *= by;
+    root *= mean < 1.0 ? 0x1p-64 : 0x1p64;
   }
   return mean > 0.0 ? (float)root : mean == 0.0 ? 0.0f : __builtin_nanf("");
 }

@@ -1,0 +1,52 @@
+"""The operators of long contexts where the cases of test_gpu_context.py do not
+reach, against the float64 definitions of oracle/paged.py with the tolerances
+derived there."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as od
+from gpu_util import banner, to_host64
+from test_gpu_decode import _i32
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def lb():
+    import bit_weight_gemm_int2_amd as b
+    b.lib()
+    return b
+
+
+# ------------------------------------------------- norms at the end of the range ---
+
+HUGE = [  # |x|, weights of the halves, cos, sin: with a subnormal factor 1 / |x| 1.017 to 1.019 of the bound
+    ("0x1.fdb0c6p+127", "0x1.c17d86p-1", "0x1.c0298cp-1", "0x1.6e638ap-1", "0x1.65a2b6p-1"),
+    ("0x1.f38c3ep+127", "0x1.c04a9ap-1", "0x1.c0128cp-1", "0x1.5a3918p-1", "0x1.793118p-1"),
+    ("0x1.fd171ap+127", "0x1.c0f11ep-1", "0x1.c03890p-1", "0x1.5c5f1ep-1", "0x1.773518p-1"),
+]
+
+
+@pytest.mark.parametrize("case", HUGE, ids=["0", "1", "2"])
+@pytest.mark.parametrize("way", ["dense", "append"])
+def test_norm_and_rotation_of_rows_beyond_2_to_126(lb, case, way):
+    """Rows whose root mean square has a subnormal FP32 inverse, of 22 bits: rotated, they
+    too are within 2^-21 of the row's largest normalised value (the rows here are the ones
+    that a model of the FP32 steps found farthest off with such an inverse)."""
+    banner(f"norm and rotation of huge rows, {way}, {case}")
+    x, w0, w1, c, s = (np.float32(float.fromhex(v)) for v in case)
+    D, half = 64, 32
+    rows = np.concatenate([np.full(half, x), np.full(half, -x)]).astype(np.float32)
+    w = np.concatenate([np.full(half, w0), np.full(half, w1)]).astype(np.float32)
+    cos, sin = (np.full((1, half), v, dtype=np.float32) for v in (c, s))
+    q, wt, ct, st = (torch.from_numpy(a).cuda() for a in (rows.reshape(1, 1, D), w, cos, sin))
+    if way == "dense":
+        got = lb.norm_rotate(q, q_norm=wt, cos=ct, sin=st, eps=0.0)
+    else:
+        zero = torch.zeros((1, 1, D), device="cuda")
+        got = lb.kv_append(zero, zero, lb.new_kv_cache(1, 1, 16, D), _i32([[0]]), _i32([0, 1]), _i32([0]), 1, q=q, cos=ct, sin=st,
+                           q_norm=wt, eps=0.0)
+    n = od.norm(rows.reshape(1, 1, D), w.astype(np.float64), 0.0)
+    want = od.rotate(n, np.zeros(1, dtype=int), cos, sin, False)
+    assert (np.abs(to_host64(got) - want) <= 2.0 ** -21 * np.abs(n).max()).all()
