@@ -52,6 +52,7 @@ class Model:
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.hq, self.h, self.d = q_heads, kv_heads, head_dim
         self.window, self.sinks = window, sinks
+        self.missing = torch.zeros(1, dtype=torch.int32, device="cuda")  # pages that the pool did not have
         self.embed = torch.randn((vocab, hidden), generator=g, device="cuda").bfloat16()
         self.layers = [dict(qkv=Linear4((q_heads + 2 * kv_heads) * head_dim, hidden, g),
                             o=Linear4(hidden, q_heads * head_dim, g), up=Linear4(2 * mlp, hidden, g),
@@ -79,10 +80,12 @@ class Model:
         return self.head(norm(x))
 
     def pages_for(self, table, lens, rows, room):
-        """A table for the sequences that go on, with room for their next tokens; copies what it asks for."""
+        """A table for the sequences that go on, with room for their next tokens; copies what it asks for. Tokens whose page the
+        pool does not have are lost: counted on the GPU, which a step does not wait for."""
         plan = lb.kv_remap(table, lens, self.layers[0]["cache"], rows=rows, room=room, window=self.window, sinks=self.sinks)
         for w in self.layers:
             lb.kv_copy_pages(w["cache"], plan.src, plan.dst, plan.counts)
+        self.missing += plan.counts[2]
         return plan.table, plan.lens
 
     def reference(self, tokens):
@@ -119,7 +122,9 @@ class Model:
 
 def generate(model, prompts, steps, width, answers=1):
     """Greedy continuations of a batch of prompts (lists of token numbers): `answers` of each, which differ in their first
-    token (the likeliest ones). Returns the sequences, the last step's logits and the seconds a step took."""
+    token (the likeliest ones). Returns the sequences, the last step's logits and the seconds a step took. A pool with too few
+    pages is an error, found at the end."""
+    model.missing.zero_()
     i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
     lens, most = [len(p) for p in prompts], max(len(p) for p in prompts)
     cu = [0]
@@ -142,6 +147,8 @@ def generate(model, prompts, steps, width, answers=1):
         out.append(logits.argmax(-1))
     torch.cuda.synchronize()
     took = (time.perf_counter() - t) / max(1, steps - 1)
+    if int(model.missing):
+        raise RuntimeError(f"the pool ran out of pages: {int(model.missing)} that the sequences needed were missing")
     tails = torch.stack(out, 1).tolist()
     return [prompts[i // answers] + t for i, t in enumerate(tails)], logits, took
 

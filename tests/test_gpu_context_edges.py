@@ -50,3 +50,33 @@ def test_norm_and_rotation_of_rows_beyond_2_to_126(lb, case, way):
     n = od.norm(rows.reshape(1, 1, D), w.astype(np.float64), 0.0)
     want = od.rotate(n, np.zeros(1, dtype=int), cos, sin, False)
     assert (np.abs(to_host64(got) - want) <= 2.0 ** -21 * np.abs(n).max()).all()
+
+
+# ------------------------------------------------------------------ the example ---
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "text_decode.py")
+    spec = importlib.util.spec_from_file_location("text_decode", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_example_says_when_its_pool_runs_out(lb):
+    """Two prompts of 20 tokens and 14 more in pages of 16 need six pages, in two answers
+    each ten (the prompts' first pages are shared): enough pages pass, fewer raise, and the
+    model goes on with shorter sequences after that."""
+    banner("example: a pool with too few pages")
+    m = _example()
+    prompts = [list(range(20)), list(range(5, 25))]
+    for pages, answers, ok in ((6, 1, True), (5, 1, False), (10, 2, True), (6, 2, False)):
+        model = m.Model(1, 128, 2, 1, 64, 128, 64, 16, pages, 48)
+        if ok:
+            seqs, _, _ = m.generate(model, prompts, 15, 3, answers)
+            assert [len(s) for s in seqs] == [35] * (2 * answers)
+        else:
+            with pytest.raises(RuntimeError, match="ran out of pages"):
+                m.generate(model, prompts, 15, 3, answers)
+            assert len(m.generate(model, [prompts[0][:3]], 2, 3)[0]) == 1
