@@ -986,19 +986,18 @@ def kv_remap(block_table: torch.Tensor, lens: torch.Tensor, cache: KVCache, rows
     need = L.lowbit_kv_remap_workspace_bytes(n, pages)
     if pairs < 0 or wide < 0 or not need:
         raise LowbitError(ERR_SHAPE, "lowbit_kv_remap")
-    own = 0                                   # the workspace's words in front of the results, where none is given
-    if workspace is None:
-        own, size = need // 4, need
+    if workspace is None:                     # memory of its own: the results outlive it, and a table is kept as long as its sequences
+        workspace, size = _new(need // 4, torch.int32, block_table, stream), need
     else:
         size = _given_workspace(workspace, need, "lowbit_kv_remap")
         if workspace.get_device() != dev:
             raise _same_device(dev, workspace=workspace)
-    made = _new(own + n * wide + n + 2 * pairs + 4, torch.int32, block_table, stream)
-    at, table, new_lens, src, dst, counts = made.split_with_sizes((own, n * wide, n, pairs, pairs, 4))
+    made = _new(n * wide + n + 2 * pairs + 4, torch.int32, block_table, stream)
+    table, new_lens, src, dst, counts = made.split_with_sizes((n * wide, n, pairs, pairs, 4))
     plan = PagePlan(table.view(n, wide), new_lens, src, dst, counts)
     _check(L.lowbit_kv_remap(block_table.data_ptr(), old, lens.data_ptr(), batch, pages, cache.page, _ptr(rows), _ptr(room), n,
                              window, sinks, compact, table.data_ptr(), wide, new_lens.data_ptr(), src.data_ptr(),
-                             dst.data_ptr(), pairs, counts.data_ptr(), (workspace if at.numel() == 0 else at).data_ptr(), size,
+                             dst.data_ptr(), pairs, counts.data_ptr(), workspace.data_ptr(), size,
                              _queue(stream, dev)), "lowbit_kv_remap")
     return plan
 

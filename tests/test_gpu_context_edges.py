@@ -52,6 +52,26 @@ def test_norm_and_rotation_of_rows_beyond_2_to_126(lb, case, way):
     assert (np.abs(to_host64(got) - want) <= 2.0 ** -21 * np.abs(n).max()).all()
 
 
+# -------------------------------------------------------------------------- pages ---
+
+@pytest.mark.parametrize("stream", [False, True])
+def test_kept_page_plans_hold_their_results_only(lb, stream):
+    """A table is kept as long as its sequences live: its memory does not grow with the pool
+    (the workspace takes 8 bytes a page, 0.8 MB here)."""
+    banner(f"memory of a page plan, stream {stream}")
+    cache = lb.new_kv_cache(100000, 1, 16, 64)
+    table = _i32(np.arange(12).reshape(3, 4))
+    s = torch.cuda.Stream() if stream else None
+    torch.cuda.synchronize()
+    for compact in (False, True):
+        plan = lb.kv_remap(table, _i32([64, 30, 50]), cache, rows=_i32([0, 0, 2, 1]), room=_i32([1, 1, 1, 1]), width=5, compact=compact,
+                           stream=s)
+        torch.cuda.synchronize()
+        assert plan.counts.tolist() == [0, 12, 0, 0] and plan.table[0].tolist() == [0, 1, 2, 3, 6] and plan.table[1, 4] == 7
+        words = sum(t.numel() for t in plan)
+        assert all(t.untyped_storage().nbytes() <= 4 * words for t in plan)
+
+
 # ------------------------------------------------------------------ the example ---
 
 def _example():
