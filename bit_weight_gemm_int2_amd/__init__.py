@@ -82,6 +82,7 @@ SIGNATURES = [
     ("lowbit_attention_sinks", _I32, [_P, _P, _I64, _P, _P, _I64, _I64, _I64, _I64, _I32, _P, _I64, _I64, _I64,
                                       _P, _I64, _I64, _P, ctypes.c_float, _I32, _I64, _I64, _P, _SZ, _P]),
     ("lowbit_attention_sinks_workspace_bytes", _SZ, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I32, _I64, _I64]),
+    ("lowbit_debug_attention_plan", _I32, [_I64, _I64, _I64, _I64, _I64, _I64, _I64, _I32, _I64, _I64, _P]),
     ("lowbit_quantize", _I32, [_I32, _P, _I64, _I64, _I64, _P, _P, _P, _P]),
 ]
 MAX_GROUP = 8
@@ -817,6 +818,26 @@ def attention(q: torch.Tensor, cache: KVCache, block_table: torch.Tensor, cu_tok
         _check(L.lowbit_attention(cache.ref, *head, T, max_tokens, max_len, _DT[dtype], *qa, Hq, *oa, _ptr(lse),
                                   scale, causal, window, _ptr(workspace), size, _queue(stream, dev)), "lowbit_attention")
     return (out, lse) if return_lse else out
+
+
+class AttentionPlan(NamedTuple):
+    """How a call of attention runs: rows of a tile (16, 128, 256), parts of
+    the context, tokens of a part, and the join of the parts (0 none, 1 several
+    rows a workgroup, 2 a workgroup a row)."""
+    tile: int
+    parts: int
+    part_tokens: int
+    join: int
+
+
+def attention_plan(batch: int, tokens: int, max_tokens: int, max_len: int, q_heads: int, kv_heads: int, head_dim: int,
+                   causal: bool = True, window: int = 0, sinks: int = 0) -> AttentionPlan:
+    """Test hook: the plan of a call of attention of these sizes
+    (lowbit_debug_attention_plan)."""
+    plan = (_I32 * 4)()
+    _check(lib().lowbit_debug_attention_plan(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, causal, window,
+                                             sinks, plan), "lowbit_debug_attention_plan")
+    return AttentionPlan(*plan)
 
 
 def norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor] = None, q_norm: Optional[torch.Tensor] = None,

@@ -35,6 +35,7 @@ hipError_t launch_kv_read(const KvReadArgs& g, hipStream_t st);
 hipError_t launch_attention(const AttnArgs& a, AttnPlan p, hipStream_t st);
 AttnPlan attention_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window, int sinks,
                         bool causal, int D, int num_cu);
+AttnJoin attention_join(int splits, int64_t total, int D);
 hipError_t launch_norm_rotate(const TurnArgs& g, hipStream_t st);
 hipError_t launch_rope_tables(const TableArgs& g, hipStream_t st);
 size_t remap_workspace(int64_t new_batch, int64_t pages);
@@ -782,17 +783,23 @@ size_t attention_bytes(int splits, int64_t tokens, int64_t q_heads, int64_t D) {
   return splits > 1 ? (size_t)splits * tokens * q_heads * (D + 2) * sizeof(float) : 0;
 }
 
-size_t attention_workspace(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len, int64_t q_heads,
-                           int64_t kv_heads, int64_t head_dim, bool causal, int64_t window, int64_t sinks) {
+// The plan of a call with these bounds; no parts for a bad shape.
+lowbit::AttnPlan bounded_plan(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len, int64_t q_heads,
+                              int64_t kv_heads, int64_t head_dim, bool causal, int64_t window, int64_t sinks) {
   if (batch < 1 || tokens < 1 || max_tokens < 1 || max_len < 0 || kv_heads < 1 || q_heads < kv_heads || window < 0 ||
-      sinks < 0 ||      batch > 65535 || tokens >= kMaxDim || q_heads > 65536 || max_len > ((int64_t)1 << 30))
-    return 0;
+      sinks < 0 || batch > 65535 || tokens >= kMaxDim || q_heads > 65536 || max_len > ((int64_t)1 << 30))
+    return {};
   int num_cu = 0;
   if (current_device(&num_cu) != LOWBIT_OK) num_cu = 256;   // no gfx950 device: the MI355X's count
+  return lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
+                                (int)std::min(window, max_len), window ? (int)std::min(sinks, max_len) : 0, causal,
+                                (int)head_dim, num_cu);
+}
+
+size_t attention_workspace(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len, int64_t q_heads,
+                           int64_t kv_heads, int64_t head_dim, bool causal, int64_t window, int64_t sinks) {
   const lowbit::AttnPlan p =
-      lowbit::attention_plan(batch, (int)kv_heads, (int)(q_heads / kv_heads), std::min(max_tokens, tokens), max_len,
-                             (int)std::min(window, max_len), window ? (int)std::min(sinks, max_len) : 0, causal,
-                             (int)head_dim, num_cu);
+      bounded_plan(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, causal, window, sinks);
   return attention_bytes(p.splits, tokens, q_heads, head_dim);
 }
 
@@ -941,6 +948,21 @@ size_t lowbit_attention_sinks_workspace_bytes(int64_t batch, int64_t tokens, int
                                               int64_t q_heads, int64_t kv_heads, int64_t head_dim, int32_t causal,
                                               int64_t window, int64_t sinks) {
   return attention_workspace(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, causal != 0, window, sinks);
+}
+
+int32_t lowbit_debug_attention_plan(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len, int64_t q_heads,
+                                    int64_t kv_heads, int64_t head_dim, int32_t causal, int64_t window, int64_t sinks,
+                                    int32_t* plan) {
+  if (!plan) return LOWBIT_ERR_NULL;
+  if (!head_size(head_dim)) return LOWBIT_ERR_SHAPE;
+  const lowbit::AttnPlan p =
+      bounded_plan(batch, tokens, max_tokens, max_len, q_heads, kv_heads, head_dim, causal != 0, window, sinks);
+  if (p.splits < 1) return LOWBIT_ERR_SHAPE;
+  plan[0] = p.few ? 16 : 32 * p.waves;
+  plan[1] = p.splits;
+  plan[2] = p.split_len;
+  plan[3] = lowbit::attention_join(p.splits, tokens * q_heads, (int)head_dim);
+  return LOWBIT_OK;
 }
 
 int32_t lowbit_norm_rotate(int32_t dtype, int64_t tokens, int64_t head_dim, const void* q, int64_t qts, int64_t qhs,

@@ -44,6 +44,8 @@
 
 namespace lowbit {
 
+AttnJoin attention_join(int splits, int64_t total, int D);
+
 namespace {
 
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
@@ -791,14 +793,17 @@ __global__ __launch_bounds__(256) void attend_join_kernel(AttnArgs a) {
   if (tid == 0) store_lse(a, token, head, m, l);
 }
 
-// The same join of up to 8 parts (as many as the kernel above has groups), to the
-// bit, where there are many rows: D / 4 threads a row, every read under way at
-// once. 1024 queries of 32 heads in two parts: 87 us with their attention, 124 with
-// a workgroup a row.
+constexpr int JOIN_ROWS = 512;
+constexpr int row_parts(int D) { return 1024 / D < 8 ? 1024 / D : 8; }   // that the join of many rows takes
+
+// The same join of up to 8 parts (4 for heads of 256: as many as the kernel above
+// has groups), to the bit, where there are many rows: D / 4 threads a row, every
+// read under way at once. 1024 queries of 32 heads in two parts: 87 us with their
+// attention, 124 with a workgroup a row.
 template <bool BF16, int D>
 __global__ __launch_bounds__(256) void attend_join_rows_kernel(AttnArgs a) {
 #pragma clang fp contract(off)                                         // the other kernel rounds products before it adds them
-  constexpr int TPR = D / 4, NG = 256 / TPR, MAX = NG < 8 ? NG : 8;
+  constexpr int TPR = D / 4, NG = 256 / TPR, MAX = row_parts(D);
   const int64_t total = a.t.tokens * a.q_heads, row = (int64_t)blockIdx.x * NG + threadIdx.x / TPR;
   const int d = threadIdx.x % TPR * 4;
   if (row >= total) return;
@@ -835,7 +840,6 @@ __global__ __launch_bounds__(256) void attend_join_rows_kernel(AttnArgs a) {
   if (d == 0) store_lse(a, token, head, m, ((l[0] + l[4]) + (l[2] + l[6])) + ((l[1] + l[5]) + (l[3] + l[7])));
 }
 
-constexpr int JOIN_ROWS = 512;
 constexpr int FEW_ROWS = 80;
 constexpr int FEW_SPLIT = 4096;            // tokens of a part that PAGES covers at pages of 16 (plus one page of offset)
 
@@ -859,7 +863,7 @@ hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
   if (a.splits > 1) {
     const int64_t total = a.t.tokens * a.q_heads, nx = std::min<int64_t>(total, 1 << 22);   // nx * 256 threads fit 32 bits
     constexpr int NG = 1024 / D;
-    if (a.splits <= std::min(NG, 8) && total >= JOIN_ROWS && total / NG < 1 << 22)
+    if (attention_join(a.splits, total, D) == JOIN_BY_ROWS)
       attend_join_rows_kernel<BF16, D><<<(unsigned)((total + NG - 1) / NG), 256, 0, st>>>(a);
     else
       attend_join_kernel<BF16, D><<<dim3((unsigned)nx, (unsigned)((total + nx - 1) / nx)), 256, 0, st>>>(a);
@@ -868,6 +872,12 @@ hipError_t launch(const AttnArgs& a, AttnPlan p, hipStream_t st) {
 }
 
 }  // namespace
+
+// How `total` rows in `splits` parts are joined. (A launch's first dimension holds 2^24 workgroups of 256 threads.)
+AttnJoin attention_join(int splits, int64_t total, int D) {
+  if (splits < 2) return JOIN_NONE;
+  return splits <= row_parts(D) && total >= JOIN_ROWS && total / (1024 / D) < 1 << 22 ? JOIN_BY_ROWS : JOIN_BY_GROUPS;
+}
 
 // Which kernel, how many waves a workgroup, and how many parts the context is
 // split into. Up to 80 rows go in tiles of 16, each reading the context again

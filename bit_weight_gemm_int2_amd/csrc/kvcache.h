@@ -123,4 +123,6 @@ struct AttnPlan {
   int splits, split_len;
 };
 
+enum AttnJoin { JOIN_NONE = 0, JOIN_BY_ROWS = 1, JOIN_BY_GROUPS = 2 };   // several rows a workgroup, or one
+
 }  // namespace lowbit

@@ -30,6 +30,7 @@
  *  - Test hook: lowbit_debug_force_variant (below) forces one kernel family
  *    so that tests reach every launch path; the environment variable
  *    LOWBIT_FORCE_VARIANT, read once per process, sets its initial value.
+ *    lowbit_debug_attention_plan tells which one attention takes.
  *
  * Packed weight layout (this library's own; the pages fix only "2 bits per
  * ternary" and "1 bit per binary weight")
@@ -631,6 +632,16 @@ int32_t lowbit_attention_sinks(const lowbit_kv_cache* cache, const int32_t* bloc
 size_t lowbit_attention_sinks_workspace_bytes(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len,
                                               int64_t q_heads, int64_t kv_heads, int64_t head_dim, int32_t causal,
                                               int64_t window, int64_t sinks);
+
+/* Test hook: how a call of lowbit_attention_sinks (or, with sinks 0,
+ * lowbit_attention) of these sizes runs on the current GPU (on one of 256 CUs
+ * where there is none), so that a test can say which kernels it reaches:
+ *   plan  host int32 [4]: rows of a tile (16, 128, 256), parts of the context,
+ *         tokens of a part, and the join of the parts (0 none, 1 several rows a
+ *         workgroup, 2 a workgroup a row) */
+int32_t lowbit_debug_attention_plan(int64_t batch, int64_t tokens, int64_t max_tokens, int64_t max_len, int64_t q_heads,
+                                    int64_t kv_heads, int64_t head_dim, int32_t causal, int64_t window, int64_t sinks,
+                                    int32_t* plan);
 
 /* Several independent linears of one shape in one launch: problem z computes
  *

@@ -335,3 +335,29 @@ def test_struct_and_signatures_hold_the_new_calls(b):
     for n in ("lowbit_kv_append_norm", "lowbit_norm_rotate", "lowbit_rope_tables", "lowbit_kv_remap", "lowbit_kv_copy_pages",
               "lowbit_attention_sinks"):
         assert n in names and isinstance(getattr(b.lib(), n), ctypes._CFuncPtr)
+
+
+def test_attention_plan(b):
+    """The test hook that names the kernels of a call agrees with the workspace that the call asks for; without a GPU it
+    plans for 256 CUs. (Refusals need no GPU.)"""
+    L = b.lib()
+    for batch, tokens, new, length, hq, h, d, causal, window, sinks in (
+            (1, 1, 1, 300, 8, 2, 128, 1, 0, 0), (4, 4, 1, 9000, 8, 1, 64, 1, 0, 0), (1, 90, 90, 4500, 1, 1, 256, 0, 0, 0),
+            (1, 4096, 4096, 20000, 32, 8, 128, 1, 2500, 70), (48, 48, 1, 16000, 40, 8, 128, 1, 4096, 20),
+            (24, 24, 1, 16000, 16, 4, 256, 1, 4000, 4), (1, 2000, 2000, 20000, 32, 8, 128, 1, 2500, 0)):
+        plan = b.attention_plan(batch, tokens, new, length, hq, h, d, causal, window, sinks)
+        assert plan.tile == (16 if new * hq // h <= 80 else plan.tile) and plan.tile in (16, 128, 256)
+        assert plan.part_tokens % 128 == 0 and plan.parts * plan.part_tokens >= min(length, window + sinks if window else length)
+        assert plan.join == (0 if plan.parts == 1 else 1 if plan.parts <= min(8, 1024 // d) and tokens * hq >= 512 else 2)
+        need = (L.lowbit_attention_sinks_workspace_bytes(batch, tokens, new, length, hq, h, d, causal, window, sinks) if sinks else
+                L.lowbit_attention_workspace_bytes(batch, tokens, new, length, hq, h, d, window))
+        assert need == (plan.parts * tokens * hq * (d + 2) * 4 if plan.parts > 1 else 0)
+    plan = (ctypes.c_int32 * 4)()
+    call = L.lowbit_debug_attention_plan
+    good = (1, 1, 1, 300, 8, 2, 128, 1, 0, 0)
+    assert call(*good, plan) == b.OK and call(*good, None) == b.ERR_NULL
+    for at, value in ((0, 0), (0, 65536), (1, 0), (1, 1 << 31), (2, 0), (3, -1), (3, (1 << 30) + 1), (4, 1), (4, 65537), (5, 0), (6, 96),
+                      (6, 0), (8, -1), (9, -1)):
+        assert call(*good[:at], value, *good[at + 1:], plan) == b.ERR_SHAPE, (at, value)
+    with pytest.raises(b.LowbitError):
+        b.attention_plan(0, 1, 1, 300, 8, 2, 128)

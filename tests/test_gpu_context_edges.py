@@ -7,7 +7,7 @@ import torch
 
 from oracle import paged as od
 from gpu_util import banner, to_host64
-from test_gpu_decode import _i32
+from test_gpu_decode import _i32, _values
 
 pytestmark = pytest.mark.gpu
 
@@ -17,6 +17,96 @@ def lb():
     import bit_weight_gemm_int2_amd as b
     b.lib()
     return b
+
+
+# ------------------------------------------------- attention by the shape of its plan ---
+
+class Long:
+    """Sequences in a cache made on the GPU, with pages in no order."""
+
+    def __init__(self, lb, lens, H, page, D, seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        self.lens, self.page, self.D = lens, page, D
+        width = -(-max(lens) // page)
+        pages = len(lens) * width + 3
+        k, v = ((torch.randn((pages, H, page, D), generator=g, device="cuda") * 36).round_().clamp_(-127, 127).add_(128)
+                .to(torch.uint8) for _ in range(2))
+        ks, vs = ((0.5 + torch.rand((pages, H), generator=g, device="cuda")) * (3.5 / 127) for _ in range(2))
+        self.cache = lb.KVCache(k, v, ks, vs)
+        self.table = torch.randperm(pages, generator=g, device="cuda")[:len(lens) * width].to(torch.int32).view(len(lens), width)
+
+    def rows(self, lb, b):
+        """Keys and values [L, H, D] and value scales [L, H] of sequence b, float64."""
+        L = self.lens[b]
+        k, v = lb.kv_read(self.cache, self.table[b:b + 1].contiguous(), _i32([0, L]), _i32([0]), L, L, torch.float32)
+        vs = self.cache.v_scale[self.table[b].long()[torch.arange(L, device="cuda") // self.page]]
+        return k.double(), v.double(), vs.double()
+
+
+def _half(y, dtype):
+    """Half a unit in the last place of y."""
+    bits, low = (8, -133) if dtype == torch.bfloat16 else (11, -24)
+    e = torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -140)))
+    return 0.5 * torch.exp2((e - bits + 1).clamp(min=low))
+
+
+def _check(lb, P, q, out, lse, cu, causal, window, sinks):
+    """Every row against float64 on the GPU: 2^-10 sum p |v| / sum p + 2^-25 tokens 127 max(p v_scale) / sum p + half an
+    output ulp, and the log of the sum within 2^-14 + 2^-22 of itself."""
+    H, group = P.cache.kv_heads, q.shape[1] // P.cache.kv_heads
+    for b in range(len(P.lens)):
+        L, n = P.lens[b], cu[b + 1] - cu[b]
+        if not n or not L:
+            assert (out[cu[b]:cu[b + 1]] == 0).all() and torch.isneginf(lse[cu[b]:cu[b + 1]]).all()
+            continue
+        k, v, vs = P.rows(lb, b)
+        pos = L - n + torch.arange(n, device="cuda").repeat_interleave(group)[:, None]
+        j = torch.arange(L, device="cuda")[None]
+        seen = (j <= pos) if causal else (j >= 0).expand(n * group, L)
+        if window:
+            seen = seen & ((j > pos - window) | (j < sinks))
+        for h in range(H):
+            rows = (slice(cu[b], cu[b + 1]), slice(h * group, (h + 1) * group))
+            s = q[rows].double().reshape(-1, P.D) @ k[:, h].t().contiguous() * P.D ** -0.5
+            s.masked_fill_(~seen, -torch.inf)
+            top = s.amax(-1, keepdim=True)
+            e = torch.exp(s - torch.where(top > -torch.inf, top, 0.0))
+            total = e.sum(-1, keepdim=True)
+            safe = torch.where(total > 0, total, 1.0)
+            want, mag = (e @ v[:, h].contiguous()) / safe, (e @ v[:, h].abs().contiguous()) / safe
+            peak = 127 * seen.sum(-1, keepdim=True) * (e * vs[:, h]).amax(-1, keepdim=True) / safe
+            got = out[rows].double().reshape(-1, P.D)
+            bound = 2.0 ** -10 * mag + 2.0 ** -25 * peak + _half(torch.maximum(want.abs(), got.abs()), out.dtype)
+            assert ((got - want).abs() <= bound).all(), (b, h, ((got - want).abs() / bound.clamp(min=1e-30)).max().item())
+            want, got = (top + torch.log(total)).flatten(), lse[rows].double().flatten()
+            none = total.flatten() == 0
+            assert torch.isneginf(got[none]).all()
+            assert ((got - want).abs()[~none] <= 2.0 ** -14 + 2.0 ** -22 * want.abs()[~none]).all()
+
+
+PLANS = [  # lens, new, H, Hq, page, D, dtype, window, sinks, (rows of a tile, parts, join), more tokens a part than a segment of pages holds
+    # 256-row tiles over several segments
+    ([12000], [1900], 8, 64, 16, 128, "bf16", 8300, 50, (256, 1, 0), True),
+    ([9000, 7777], [2048, 1000], 8, 64, 32, 128, "f16", 5000, 333, (256, 1, 0), False),
+    # 128-row tiles over two segments, the first with the gap
+    ([6200], [130], 8, 512, 16, 64, "bf16", 4500, 100, (128, 1, 0), True),
+]
+
+
+@pytest.mark.parametrize("case", PLANS, ids=[str(i) for i in range(len(PLANS))])
+def test_attention_sinks_by_plan(lb, case):
+    """Shapes that are planned as stated (on 256 CUs), each row against float64."""
+    lens, new, H, Hq, page, D, dt, window, sinks, plan, segments = case
+    banner(f"attention with first tokens as planned {case}")
+    T, cu = sum(new), [0, *np.cumsum(new).tolist()]
+    got = lb.attention_plan(len(lens), T, max(new), max(lens), Hq, H, D, True, window, sinks)
+    assert (got.tile, got.parts, got.join) == plan
+    assert (got.part_tokens > 256 * page) == segments          # of pages that the LDS holds at a time
+    P = Long(lb, lens, H, page, D, seed=D + page)
+    q = 6 * _values(np.random.default_rng(T), (T, Hq, D), dt)[0]    # a few tokens rule each row: one too many or too few shows
+    out, lse = lb.attention(q, P.cache, P.table, _i32(cu), _i32(lens), max(new), max(lens), window=window, sinks=sinks,
+                            return_lse=True)
+    _check(lb, P, q, out, lse, cu, True, window, sinks)
 
 
 # ------------------------------------------------- norms at the end of the range ---
