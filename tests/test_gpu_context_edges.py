@@ -109,6 +109,51 @@ def test_attention_sinks_by_plan(lb, case):
     _check(lb, P, q, out, lse, cu, True, window, sinks)
 
 
+JOINS = [  # lens, new, H, Hq, D, window, sinks, parts
+    ([2500], [90], 1, 1, 64, 0, 0, 2),
+    ([9000], [90], 1, 1, 64, 0, 0, 8),
+    ([3000], [90], 1, 2, 64, 2500, 30, 5),
+    ([3400], [90], 1, 1, 128, 0, 0, 3),
+    ([7800], [90], 1, 1, 128, 0, 0, 7),
+    ([3000], [90], 1, 2, 128, 2500, 30, 5),
+    ([2500], [90], 1, 1, 256, 0, 0, 2),
+    ([4500], [90], 1, 1, 256, 0, 0, 4),
+    ([1400, 1000, 900, 10, 0, 600, 904, 1399], [1] * 8, 1, 4, 256, 900, 4, 4),
+]
+
+
+@pytest.mark.parametrize("case", JOINS, ids=[str(i) for i in range(len(JOINS))])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_the_two_joins_give_the_same_bits(lb, case, dt):
+    """The same queries in a batch of fewer than 512 rows, whose parts one workgroup a row
+    joins, and padded to more with rows of no sequence, where groups of threads do."""
+    lens, new, H, Hq, D, window, sinks, parts = case
+    banner(f"the two joins of {parts} parts, heads of {D}, {case} {dt}")
+    T, B, most, longest = sum(new), len(lens), max(new), max(lens)
+    more = T + 600 // Hq
+    a, b = (lb.attention_plan(B, t, most, longest, Hq, H, D, True, window, sinks) for t in (T, more))
+    assert a[:3] == b[:3] and a.parts == parts and (a.join, b.join) == (2, 1) and T * Hq < 512 <= more * Hq
+    P, cu = Long(lb, lens, H, 16, D, seed=parts), [0, *np.cumsum(new).tolist()]
+    q, _ = _values(np.random.default_rng(D + parts), (more, Hq, D), dt)
+    call = lambda x: lb.attention(x, P.cache, P.table, _i32(cu), _i32(lens), most, longest, window=window, sinks=sinks,  # noqa: E731
+                                  return_lse=True)
+    (out, lse), (wide, wide_lse) = call(q[:T].contiguous()), call(q)
+    assert torch.equal(out, wide[:T]) and torch.equal(lse, wide_lse[:T])
+    _check(lb, P, q, out, lse, cu, True, window, sinks)
+
+
+def test_the_join_by_rows_of_heads_of_256(lb):
+    """Parts of two ragged sequences, joined by rows; the second one's later parts hold nothing."""
+    lens, new, window, sinks = [2500, 20], [300, 20], 1500, 50
+    banner("join by rows, heads of 256")
+    assert lb.attention_plan(2, 320, 300, 2500, 2, 1, 256, True, window, sinks)[1:] == (3, 640, 1)
+    P, cu = Long(lb, lens, 1, 16, 256, seed=21), [0, 300, 320]
+    for dt in ("bf16", "f16"):
+        q, _ = _values(np.random.default_rng(22), (320, 2, 256), dt)
+        out, lse = lb.attention(q, P.cache, P.table, _i32(cu), _i32(lens), 300, 2500, window=window, sinks=sinks, return_lse=True)
+        _check(lb, P, q, out, lse, cu, True, window, sinks)
+
+
 # ------------------------------------------------- norms at the end of the range ---
 
 HUGE = [  # |x|, weights of the halves, cos, sin: with a subnormal factor 1 / |x| 1.017 to 1.019 of the bound
