@@ -154,6 +154,34 @@ def test_the_join_by_rows_of_heads_of_256(lb):
         _check(lb, P, q, out, lse, cu, True, window, sinks)
 
 
+BIG = [  # rows of the batch, queries, length, (parts, join): more than a launch's first dimension holds
+    (2 ** 22 + 100, 60, 1500, (6, 2)),        # more parts than the join by rows takes: both dimensions of the other one
+    (2 ** 24 + 100, 100, 2500, (2, 2)),       # more rows than the join by rows takes
+]
+
+
+@pytest.mark.parametrize("rows,n,L,plan", BIG, ids=["parts", "rows"])
+def test_joins_of_more_rows_than_one_grid_dimension_holds(lb, rows, n, L, plan):
+    """One sequence's queries at the end of a batch of rows of no sequence (which stay as they
+    are): the same bits as without them."""
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 80 << 30:
+        pytest.skip("needs 80 GiB of free GPU memory")
+    banner(f"join of {rows} rows of 256 in {plan[0]} parts")
+    P = Long(lb, [L], 1, 16, 256, seed=31)
+    assert lb.attention_plan(1, rows, n, L, 1, 1, 256)[1::2] == plan
+    x, _ = _values(np.random.default_rng(32), (n, 1, 256), "bf16")
+    q = torch.zeros((rows, 1, 256), dtype=torch.bfloat16, device="cuda")
+    q[-n:] = x
+    out = torch.full((rows, 1, 256), 7.0, dtype=torch.bfloat16, device="cuda")
+    lb.attention(q, P.cache, P.table, _i32([rows - n, rows]), _i32([L]), n, L, out=out)
+    want, lse = lb.attention(x, P.cache, P.table, _i32([0, n]), _i32([L]), n, L, return_lse=True)
+    assert torch.equal(out[-n:], want) and (out[:-n] == 7.0).all()
+    _check(lb, P, x, want, lse, [0, n], True, 0, 0)
+    del q, out
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------- norms at the end of the range ---
 
 HUGE = [  # |x|, weights of the halves, cos, sin: with a subnormal factor 1 / |x| 1.017 to 1.019 of the bound
