@@ -90,6 +90,12 @@ PLANS = [  # lens, new, H, Hq, page, D, dtype, window, sinks, (rows of a tile, p
     ([9000, 7777], [2048, 1000], 8, 64, 32, 128, "f16", 5000, 333, (256, 1, 0), False),
     # 128-row tiles over two segments, the first with the gap
     ([6200], [130], 8, 512, 16, 64, "bf16", 4500, 100, (128, 1, 0), True),
+    # 16-row tiles in parts: several tiles a sequence and head, and heads of 256
+    ([4000 - 300 * i for i in range(8)], [16] * 8, 1, 5, 16, 128, "bf16", 2500, 20, (16, 6, 1), False),
+    ([5000, 3100, 40], [10, 9, 10], 1, 8, 64, 64, "f16", 3000, 33, (16, 13, 2), False),
+    ([3000, 1900], [80, 41], 1, 1, 16, 256, "f16", 2000, 40, (16, 9, 2), False),
+    ([8000 - 200 * i for i in range(24)], [1] * 24, 4, 16, 32, 256, "bf16", 4000, 4, (16, 8, 2), False),
+    ([9000, 6100, 6000, 100, 5], [1] * 5, 1, 2, 16, 256, "f16", 6000, 100, (16, 24, 2), False),
 ]
 
 
