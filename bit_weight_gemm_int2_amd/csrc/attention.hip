@@ -924,7 +924,7 @@ static AttnPlan window_plan(int64_t batch, int heads, int group, int64_t max_tok
       const int64_t round = (int64_t)s.most * num_cu, rest = tiles * n % round;
       double us = tiles * n / round * (s.fixed + s.step[s.most - 1] * steps);
       if (rest) us += s.fixed + s.step[(rest - 1) / num_cu] * steps;
-      if (n > 1) us += 6.0 + 1e-3 * (0.2 + 0.25 * n + (n > 1024 / D ? 1.6 : 0.0)) * D / 128 * batch * rows * heads;
+      if (n > 1) us += 6.0 + 1e-3 * (0.2 + 0.25 * n + (n > row_parts(D) ? 1.6 : 0.0)) * D / 128 * batch * rows * heads;
       if (us < least) {
         least = us;
         best.waves = W;
@@ -941,7 +941,8 @@ static AttnPlan window_plan(int64_t batch, int heads, int group, int64_t max_tok
 // the others decides. The number of parts that a time estimate likes best: 2 us, a
 // step of 128 tokens 0.9 us or its bytes at 30 GB/s a CU for the CUs with the most
 // workgroups, or at 7 TB/s as if all had as many; parts cost 4 us, 0.02 us each and
-// 0.4 us a thousand rows and part (2 us a thousand more where a workgroup joins each), and
+// 0.4 us a thousand rows and part (2 us a thousand more where a workgroup joins each: over 8
+// parts, over 4 with heads of 256 and 512 rows), and
 // no call from a host takes less than 12 us, 16 with a second launch (one sequence and
 // a window of 1000: 10.7 us whole and 9.7 in parts on the GPU, 12.3 and 16 as calls).
 // Over 150 shapes within 2 % of the best number on average (the rule for ragged
@@ -953,6 +954,7 @@ static AttnPlan few_window_plan(int64_t batch, int heads, int group, int64_t max
   const int64_t span = std::min(max_len, window + max_tokens + 16 + (sinks + 15) / 16 * 16);
   const int64_t least = std::max<int64_t>(1, (span + FEW_SPLIT - 1) / FEW_SPLIT);
   const double bytes = 256.0 * D;
+  const int most = all < JOIN_ROWS ? 8 : row_parts(D);       // parts without the dearer join
   AttnPlan best{};
   best.few = true;
   best.waves = 4;
@@ -963,7 +965,7 @@ static AttnPlan few_window_plan(int64_t batch, int heads, int group, int64_t max
     const int64_t turns = (wgs + num_cu - 1) / num_cu, even = wgs <= num_cu ? wgs : turns * num_cu;
     const double step = std::max({0.9, turns * bytes / 3.0e4, even * bytes / 7.0e6});
     double us = 2.0 + step * (len / 128);
-    if (parts > 1) us += 4.0 + 0.02 * parts + 1e-3 * all * (0.4 * parts * D / 128 + (parts > 8 ? 2.0 : 0.0));
+    if (parts > 1) us += 4.0 + 0.02 * parts + 1e-3 * all * (0.4 * parts * D / 128 + (parts > most ? 2.0 : 0.0));
     us = std::max(us, parts > 1 ? 16.0 : 12.0) + 1e-3 * us;
     if (us < shortest) {
       shortest = us;

@@ -361,3 +361,11 @@ def test_attention_plan(b):
         assert call(*good[:at], value, *good[at + 1:], plan) == b.ERR_SHAPE, (at, value)
     with pytest.raises(b.LowbitError):
         b.attention_plan(0, 1, 1, 300, 8, 2, 128)
+
+
+@pytest.mark.parametrize("window,parts", [(4000, 4), (1000, 3)])
+def test_plan_of_few_rows_knows_which_join_heads_of_256_take(b, window, parts):
+    """Where 5 parts with a workgroup a row to join and 3 or 4 joined by rows come out nearly alike, the dearer join counts
+    (48 sequences of 16 heads; on 256 CUs)."""
+    plan = b.attention_plan(48, 48, 1, 4 * window, 16, 1, 256, True, window, 4)
+    assert plan.join == 1 and plan.parts == parts
