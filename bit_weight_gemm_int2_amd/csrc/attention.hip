@@ -20,7 +20,10 @@
 //    cache, with the accumulators rescaled only when a maximum grows.
 //  * FP16 probabilities: each is off by at most 2^-11, independently, so the
 //    result by about 2^-12, less than a BF16 output's rounding (2^-9) and as
-//    much as an FP16 one's; FP32 ones would double the matrix instructions.
+//    much as an FP16 one's (against 64 bits, FP16 results are 5 to 8 % farther
+//    off than with FP32 probabilities, 2.19e-4 to 2.08e-4 of the norm for 48
+//    sequences and a window of 4096, BF16 ones below 1 %); FP32 ones would
+//    double the matrix instructions.
 //    They carry a factor of 2^TOP that puts the largest near the top of FP16's
 //    range, so that tokens of 2^-28 of it (2^-23 for many rows) still have full
 //    precision: where one token holds nearly all of the sum and has small
@@ -893,6 +896,8 @@ AttnJoin attention_join(int splits, int64_t total, int D) {
 // Many rows: parts until the row tiles fill the GPU twice.
 // Many rows with a window and first tokens: row tiles are of equal length, that of
 // the window and of the tile's own tokens, so whole rounds of workgroups decide.
+// (Tiles of prompts that begin within their window are shorter, the first ones most.
+// The estimate takes them at full length, and was not measured on such prompts.)
 // The shape and the number of parts that a time estimate likes best: `fixed` us a
 // workgroup and, a step of 64 tokens, `step` us with one, two or three workgroups a
 // CU; parts cost 6 us and, a thousand rows, 0.2 and 0.25 a part. 32 query heads of
@@ -942,12 +947,15 @@ static AttnPlan window_plan(int64_t batch, int heads, int group, int64_t max_tok
 // step of 128 tokens 0.9 us or its bytes at 30 GB/s a CU for the CUs with the most
 // workgroups, or at 7 TB/s as if all had as many; parts cost 4 us, 0.02 us each and
 // 0.4 us a thousand rows and part (2 us a thousand more where a workgroup joins each: over 8
-// parts, over 4 with heads of 256 and 512 rows), and
-// no call from a host takes less than 12 us, 16 with a second launch (one sequence and
-// a window of 1000: 10.7 us whole and 9.7 in parts on the GPU, 12.3 and 16 as calls).
-// Over 150 shapes within 2 % of the best number on average (the rule for ragged
-// lengths below 4 %): 24 sequences of 32 query heads and a window of 4000 42 us in four
-// parts (46 in three), with heads of 256 and 16 query heads 40 in eight (50 in three).
+// parts, over 4 with heads of 256 and 512 rows), and no call from a host takes less than
+// 12 us, 16 with a second launch (one sequence and a window of 1000: 10.7 us whole and 9.7
+// in parts on the GPU, 12.3 and 16 as calls). 24 sequences of 32 query heads and a window of
+// 4000 take 42 us in four parts (46 in three), with heads of 256 and 16 query heads 40 in
+// eight (50 in three). The host's part of the estimate costs calls that a graph replays:
+// on the GPU alone the number chosen is 4.1 % off the best of 1 to 16 on average over 135
+// shapes (1 to 64 sequences, windows of 500 to 8000, heads of 64, 128 and 256) and 41 % at
+// worst (4 sequences, window of 1000: 15.6 us whole, 11.1 in parts), without that part 1.8
+// and 15 %, with the rule for ragged lengths below 2.9 and 21 %.
 static AttnPlan few_window_plan(int64_t batch, int heads, int group, int64_t max_tokens, int64_t max_len, int window,
                                 int sinks, int D, int num_cu) {
   const int64_t rows = max_tokens * group, tiles = batch * heads * ((rows + 15) / 16), all = batch * rows * heads;

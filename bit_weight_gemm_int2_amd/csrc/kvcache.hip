@@ -2,9 +2,9 @@
 //
 // Append: key rows are rotated by their position (pairs (x, y) of the first
 // `rot` dimensions become (x cos - y sin, x sin + y cos)), after the norm of
-// the head where one is given; values are taken as they are. A block's scale is s = max(s_old, a / 127) with a the largest
-// magnitude among the block's new values (s_old = 0 for a block that starts
-// with this call), and a value r is stored as 128 + rint(r / s). When the
+// the head where one is given; values are taken as they are. A block's scale is
+// s = max(s_old, a / 127) with a the largest magnitude among the block's new
+// values (s_old = 0 for a block that starts with this call), and a value r is stored as 128 + rint(r / s). When the
 // scale grows, the block's older codes c follow it as rint(c s_old / s): each
 // growth costs them at most half a step of the new scale. The quotients are
 // real ones, so that ties (r = a / 2 is one) go to even: a bare product with

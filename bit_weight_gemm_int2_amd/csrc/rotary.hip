@@ -15,10 +15,13 @@ namespace {
 // position is one addition (an FP32 product at position 100000 would be off by
 // thousandths of a turn). The nearest quarter turn comes off its upper half, and
 // the rest, at most 1/8 turn to 2^-32, becomes FP32. Its sine and cosine are their
-// Taylor series to x^9 and x^10, which leave out less than 2e-9 at x = pi/4. A
+// Taylor series to x^9 and x^10, which leave out less than 2e-9 at x = pi/4. FP32
+// there is a choice: entries are up to 1.2e-7 off (1.4 times the RMS error of the
+// 64-bit value rounded once, up to 5.2e-8), a quarter of the contract's 2^-21. A
 // thread writes 16 bytes of each table for ROWS positions, a wave whole kilobytes,
-// past the caches; bound by the stores (131072 positions of 64 pairs: 13.6 us, 4.9
-// TB/s; 1, 4 or 8 positions a thread 14.8, 13.8 and 13.9).
+// past the caches; bound by the stores (131072 positions of 64 pairs: 12.3 to 12.9
+// us, 5.2 to 5.5 TB/s; an earlier form of 13.6 us took 14.8, 13.8 and 13.9 with 1, 4
+// or 8 positions a thread).
 constexpr int ROWS = 2;
 
 __global__ __launch_bounds__(256) void tables_kernel(TableArgs g) {

@@ -112,8 +112,8 @@ __device__ __forceinline__ double other_lane(double x) {
 // values in each of the U = D / 16 lanes that hold it (a power of two,
 // consecutive lanes, all active). The squares and their sum are FP64: no FP32
 // value overflows or vanishes there (squares of BF16 values of 2^64 pass FP32's
-// range), and it took no longer than FP32 (28.5 us for 4608 tokens of 48 heads
-// both ways). With a sum of 0 and no eps the row stays 0. The factor of a row of
+// range), and it took no longer than FP32 (both 28.5 us for 4608 tokens of 48
+// heads, in an earlier form of the dense kernel, which takes 24.5 now). With a sum of 0 and no eps the row stays 0. The factor of a row of
 // subnormal values without eps passes FP32's range (2^149 of 2^-149), and that of a
 // row beyond 2^126 is subnormal itself, with 22 bits or fewer: a row whose mean is
 // below 2^-252 or above 2^252 is moved up or down by 2^64 first, so that the factor
