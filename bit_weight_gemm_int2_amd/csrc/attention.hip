@@ -20,10 +20,11 @@
 //    cache, with the accumulators rescaled only when a maximum grows.
 //  * FP16 probabilities: each is off by at most 2^-11, independently, so the
 //    result by about 2^-12, less than a BF16 output's rounding (2^-9) and as
-//    much as an FP16 one's (against 64 bits, FP16 results are 5 to 8 % farther
-//    off than with FP32 probabilities, 2.19e-4 to 2.08e-4 of the norm for 48
-//    sequences and a window of 4096, BF16 ones below 1 %); FP32 ones would
-//    double the matrix instructions.
+//    much as an FP16 one's; FP32 ones would double the matrix instructions.
+//    Against 64 bits, FP16 results are 2 to 8 % farther off by them with few
+//    rows (2.2e-4 of the norm, 2.1e-4 with FP32 ones; a part's largest one is a
+//    power of two, and exact) and 22 to 33 % with many rows (2.5e-4 to 2.8e-4;
+//    the maximum lags there), BF16 ones below 1 %.
 //    They carry a factor of 2^TOP that puts the largest near the top of FP16's
 //    range, so that tokens of 2^-28 of it (2^-23 for many rows) still have full
 //    precision: where one token holds nearly all of the sum and has small
